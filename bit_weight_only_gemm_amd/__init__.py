@@ -11,6 +11,10 @@ Typical flow (weights quantized at load time, repacked once, then many calls):
     qw, sc, qz = w4a16_quantize_rtn(W, group_size=128, g_idx=g_idx, perm=perm)
     packed = w4a16_repack(qw, sc, qz, g_idx)       # dict of device tensors
     y = w4a16_gemm(x, packed)                      # y = x @ dequant(W)^T
+
+Beside the weight-only products: w8a8_* (products of 8-bit integers with a
+scale per token and per channel, w8a8.py) and kv8_* (a paged key/value cache
+in 8 bits, the append that fills it and the attention that reads it, kv8.py).
 """
 
 import ctypes
@@ -370,3 +374,8 @@ def _ws_cache(device, nbytes, stream=None):
         cur = workspace(max(nbytes, 1 << 20), device)
         _WS[key] = cur
     return cur
+
+
+from .kv8 import (kv8_append, kv8_attention, kv8_attention_workspace_bytes,  # noqa: E402,F401
+                  kv8_cache, kv8_dequant)
+from .w8a8 import w8a8_gemm, w8a8_linear, w8a8_quantize, w8a8_workspace_bytes  # noqa: E402,F401

@@ -50,6 +50,19 @@ SIGNATURES = {
     "w4a16_stream_read": (_c.c_int, [_p, _i64, _i32, _p, _p]),
     "w4a16_gemm_noalloc": (_c.c_int, [_p, _p, _p, _p, _p, _p, _i32, _i32, _p, _i64, _i64, _i64,
                                       _i32, _p]),
+    "w8a8_quantize": (_c.c_int, [_p, _i64, _i64, _i64, _i32, _p, _p, _p]),
+    "w8a8_workspace_bytes": (_i64, [_i64, _i64, _i64, _i32]),
+    "w8a8_gemm": (_c.c_int, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p]),
+    "w8a8_linear": (_c.c_int, [_p, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p]),
+    "kv8_append": (_c.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _i32,
+                              _p, _i64, _p, _p, _p, _p, _i64, _i32, _i32, _i64, _i64, _i64, _i32,
+                              _i32, _i32, _i32, _p]),
+    "kv8_dequant": (_c.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _p, _i64, _i32, _p, _p,
+                               _p]),
+    "kv8_attention_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64, _i32, _i32, _i32]),
+    "kv8_attention": (_c.c_int, [_p, _i64, _p, _p, _p, _p, _i64, _i32, _p, _i64, _p, _p,
+                                 _c.c_float, _i32, _p, _i64, _p, _i64, _i64, _i64, _i64, _i32,
+                                 _i32, _i32, _i32, _p, _i64, _p]),
 }
 
 _lib = None

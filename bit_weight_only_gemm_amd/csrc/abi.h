@@ -1,0 +1,61 @@
+// abi.h -- what the C entry points share: pointer checks, the status of a HIP
+// call, and the guard that keeps C++ exceptions inside the library.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <cstring>
+#include <initializer_list>
+
+#include "../../include/w4a16.h"
+
+namespace w4a16 {
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+inline int check_ptrs(std::initializer_list<const void*> required) {
+  for (const void* p : required) {
+    if (!p) return W4A16_ERR_INVALID_ARG;
+  }
+  for (const void* p : required) {
+    if (!aligned16(p)) return W4A16_ERR_MISALIGNED;
+  }
+  return W4A16_OK;
+}
+
+inline int hip_status(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
+
+// The launchers report hipGetLastError() after their launches; an error an
+// earlier runtime call of the caller left pending is cleared (consumed) first
+// so that it is not reported as this call's failure.
+inline void clear_pending_error() { (void)hipGetLastError(); }
+
+// Runs an entry point's body so that no C++ exception crosses the C ABI: a
+// failed host allocation (std::bad_alloc) or any other exception becomes
+// W4A16_ERR_HOST.
+template <class F>
+int guarded(F&& f) noexcept {
+  try {
+    return f();
+  } catch (...) {
+    return W4A16_ERR_HOST;
+  }
+}
+
+inline int validate_dtype(int32_t dtype) {
+  return (dtype == W4A16_F16 || dtype == W4A16_BF16) ? W4A16_OK : W4A16_ERR_INVALID_ARG;
+}
+
+// Copies a plan's text to a caller's buffer, truncated to fit and terminated;
+// its full length.
+inline int64_t copy_names(const char* s, char* names_host, int64_t names_bytes) {
+  const int64_t len = (int64_t)std::strlen(s);
+  if (names_bytes > 0) {
+    const int64_t n = len < names_bytes - 1 ? len : names_bytes - 1;
+    std::memcpy(names_host, s, (size_t)n);
+    names_host[n] = 0;
+  }
+  return len;
+}
+
+}  // namespace w4a16

@@ -11,7 +11,7 @@
 #include <mutex>
 #include <vector>
 
-#include "../../include/w4a16.h"
+#include "abi.h"
 #include "common.h"
 #include "kernels.h"
 
@@ -22,37 +22,6 @@ static_assert(kScratchBytes == W4A16_NOALLOC_SCRATCH_BYTES, "the header states t
 namespace {
 
 constexpr int64_t kMaxM = (int64_t)1 << 21;  // keeps every row-block grid dimension < 65536
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-int check_ptrs(std::initializer_list<const void*> required) {
-  for (const void* p : required) {
-    if (!p) return W4A16_ERR_INVALID_ARG;
-  }
-  for (const void* p : required) {
-    if (!aligned16(p)) return W4A16_ERR_MISALIGNED;
-  }
-  return W4A16_OK;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
-
-// The launchers report hipGetLastError() after their launches; an error an
-// earlier runtime call of the caller left pending is cleared (consumed) first
-// so that it is not reported as this call's failure.
-void clear_pending_error() { (void)hipGetLastError(); }
-
-// Runs an entry point's body so that no C++ exception crosses the C ABI: a
-// failed host allocation (std::bad_alloc) or any other exception becomes
-// W4A16_ERR_HOST.
-template <class F>
-int guarded(F&& f) noexcept {
-  try {
-    return f();
-  } catch (...) {
-    return W4A16_ERR_HOST;
-  }
-}
 
 // ---- NF4 codebook, computed here from its closed form (independent of any
 // table elsewhere): Phi^-1 by Newton iteration on erfc in double precision.
@@ -129,10 +98,6 @@ int validate_bits(int32_t bits) {
 }
 int validate_zero_rows(int64_t N, int32_t bits, bool zeros) {
   return (zeros && bits == 3 && N % 32 != 0) ? W4A16_ERR_INVALID_ARG : W4A16_OK;
-}
-
-int validate_dtype(int32_t dtype) {
-  return (dtype == W4A16_F16 || dtype == W4A16_BF16) ? W4A16_OK : W4A16_ERR_INVALID_ARG;
 }
 
 }  // namespace

@@ -1,0 +1,162 @@
+"""A paged key/value cache in 8 bits, one scale per (page, kv head): the append
+that fills it and the attention that reads it (the ``kv8_*`` entry points of
+``include/w4a16.h``).
+
+    cache = kv8_cache(num_pages, 64, kv_heads, head_dim)
+    q = kv8_append(cache, k, v, page_table, seq_lens, q=q, cos=cos, sin=sin)
+    o = kv8_attention(q, cache, page_table, seq_lens)
+
+page_table int32 [B, max_pages], seq_lens int32 [B] (the new tokens included)
+and cu_seqlens int32 [B + 1] stay on the device; without cu_seqlens each
+sequence has one new token.  Rows of q, k and v are [tokens, heads, D] and may
+be slices of a fused projection.
+"""
+
+import math
+
+import torch
+
+from . import _DT, _lib, _need, _ptr, _stream
+from .w8a8 import _empty, _space
+
+
+def kv8_cache(num_pages, page_size, kv_heads, head_dim, device="cuda"):
+    """An empty cache: dict(k, v, k_scale, v_scale, page_size, kv_heads,
+    head_dim, num_pages); k uint8 [pages, Hkv, T, D], v uint8 [pages, Hkv,
+    T / 16, D, 16], a code c standing for (c - 128) * scale [pages, Hkv]."""
+    T, D = page_size, head_dim
+    if T not in (16, 32, 64, 128) or D not in (64, 128):
+        raise _lib.W4A16Error("kv8_cache: unsupported page_size %d or head_dim %d" % (T, D))
+    n = (num_pages, kv_heads)
+    return {"k": torch.full((*n, T, D), 128, dtype=torch.uint8, device=device),
+            "v": torch.full((*n, T // 16, D, 16), 128, dtype=torch.uint8, device=device),
+            "k_scale": torch.zeros(n, device=device), "v_scale": torch.zeros(n, device=device),
+            "page_size": T, "kv_heads": kv_heads, "head_dim": D, "num_pages": num_pages}
+
+
+def _cache(c):
+    pages, Hkv, T, D = c["num_pages"], c["kv_heads"], c["page_size"], c["head_dim"]
+    _need(c["k"], torch.uint8, "cache k", pages * Hkv * T * D)
+    _need(c["v"], torch.uint8, "cache v", pages * Hkv * T * D)
+    _need(c["k_scale"], torch.float32, "cache k_scale", pages * Hkv)
+    _need(c["v_scale"], torch.float32, "cache v_scale", pages * Hkv)
+    return pages, Hkv, T, D
+
+
+def _heads(t, dtype, name, tokens=None, heads=None, D=None):
+    """Checks rows [tokens, heads, D], contiguous within a token; the row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype not in _DT or (dtype is not None and t.dtype != dtype):
+        raise TypeError("%s must be %s, got %s" % (name, dtype or "float16 or bfloat16", t.dtype))
+    if t.dim() != 3:
+        raise ValueError("%s must be [tokens, heads, D]" % name)
+    want = (t.shape[0] if tokens is None else tokens, t.shape[1] if heads is None else heads, D)
+    if tuple(t.shape) != want:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), want))
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError("%s must be contiguous within a token" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+def _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens):
+    _need(page_table, torch.int32, "page_table")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, width = page_table.shape
+    _need(seq_lens, torch.int32, "seq_lens", B)
+    if cu_seqlens is None:
+        if tokens != B:
+            raise ValueError("%d tokens for %d sequences: pass cu_seqlens" % (tokens, B))
+        return B, width, 1 if B else 0
+    _need(cu_seqlens, torch.int32, "cu_seqlens", B + 1)
+    return B, width, tokens if max_new is None else min(int(max_new), tokens)
+
+
+def kv8_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, max_new=None, q=None,
+               cos=None, sin=None, interleaved=False, q_out=None, stream=None):
+    """Appends k, v [tokens, Hkv, D] to the cache, the keys rotated by their
+    positions (cos, sin fp32 [positions, rope_dim / 2]), and returns the
+    rotated queries q [tokens, H, D] (None without q).  max_new: an upper bound
+    of the new tokens of one sequence (all of them when not given)."""
+    pages, Hkv, T, D = _cache(cache)
+    k_stride = _heads(k, None, "k", None, Hkv, D)
+    tokens = k.shape[0]
+    v_stride = _heads(v, k.dtype, "v", tokens, Hkv, D)
+    B, width, max_new = _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens)
+    H, q_stride, o_stride = Hkv, 0, 0
+    if q is not None:
+        q_stride = _heads(q, k.dtype, "q", tokens, None, D)
+        H = q.shape[1]
+        if q_out is None:
+            q_out = _empty((tokens, H, D), q.dtype, q.device, stream)
+        o_stride = _heads(q_out, k.dtype, "q_out", tokens, H, D)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rows = dim = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        _need(cos, torch.float32, "cos")
+        _need(sin, torch.float32, "sin", cos.numel())
+        if cos.dim() != 2:
+            raise ValueError("cos must be [positions, rope_dim / 2]")
+        rows, dim = cos.shape[0], 2 * cos.shape[1]
+    _lib.check(_lib.lib().kv8_append(
+        _ptr(q), q_stride, _ptr(q_out), o_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+        _ptr(cache["k"]), _ptr(cache["v"]), _ptr(cache["k_scale"]), _ptr(cache["v_scale"]), pages,
+        T, _ptr(page_table), width, _ptr(seq_lens), _ptr(cu_seqlens), _ptr(cos), _ptr(sin), rows,
+        dim, int(interleaved), tokens, B, max_new, H, Hkv, D, _DT[k.dtype], _stream(stream)),
+        "kv8_append")
+    return q_out
+
+
+def kv8_dequant(cache, pages, dtype=torch.bfloat16, stream=None):
+    """The values of pages (int32 [n]) of the cache: k, v [n, Hkv, T, D]."""
+    num, Hkv, T, D = _cache(cache)
+    if dtype not in _DT:
+        raise TypeError("dtype must be float16 or bfloat16")
+    _need(pages, torch.int32, "pages")
+    n = pages.numel()
+    k = _empty((n, Hkv, T, D), dtype, pages.device, stream)
+    v = _empty((n, Hkv, T, D), dtype, pages.device, stream)
+    _lib.check(_lib.lib().kv8_dequant(
+        _ptr(cache["k"]), _ptr(cache["v"]), _ptr(cache["k_scale"]), _ptr(cache["v_scale"]), num, T,
+        Hkv, D, _ptr(pages), n, _DT[dtype], _ptr(k), _ptr(v), _stream(stream)), "kv8_dequant")
+    return k, v
+
+
+def kv8_attention_workspace_bytes(tokens, B, max_new, max_len, heads, kv_heads, head_dim):
+    n = int(_lib.lib().kv8_attention_workspace_bytes(tokens, B, max_new, max_len, heads, kv_heads,
+                                                     head_dim))
+    if n < 0:
+        raise _lib.W4A16Error("kv8_attention_workspace_bytes: invalid sizes")
+    return n
+
+
+def kv8_attention(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None, max_len=None,
+                  scale=None, causal=True, out=None, lse=None, workspace=None, stream=None):
+    """Attention of q [tokens, H, D] over the cached tokens of their sequences:
+    [tokens, H, D] in q's dtype.  scale: 1 / sqrt(D) when not given; max_new,
+    max_len: upper bounds of the new tokens and of the length of one sequence
+    (all tokens, the table's width); lse: fp32 [tokens, H], written if given."""
+    pages, Hkv, T, D = _cache(cache)
+    q_stride = _heads(q, None, "q", None, None, D)
+    tokens, H = q.shape[0], q.shape[1]
+    B, width, max_new = _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens)
+    max_len = width * T if max_len is None else min(int(max_len), width * T)
+    if out is None:
+        out = _empty((tokens, H, D), q.dtype, q.device, stream)
+    o_stride = _heads(out, q.dtype, "out", tokens, H, D)
+    if lse is not None:
+        _need(lse, torch.float32, "lse", tokens * H)
+    L = _lib.lib()
+    need = max(0, int(L.kv8_attention_workspace_bytes(tokens, B, max_new, max_len, H, Hkv, D)))
+    workspace, nbytes = _space(workspace, need, q.device, stream)
+    _lib.check(L.kv8_attention(
+        _ptr(q), q_stride, _ptr(cache["k"]), _ptr(cache["v"]), _ptr(cache["k_scale"]),
+        _ptr(cache["v_scale"]), pages, T, _ptr(page_table), width, _ptr(seq_lens),
+        _ptr(cu_seqlens), 1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
+        _ptr(out), o_stride, _ptr(lse), tokens, B, max_new, max_len, H, Hkv, D, _DT[q.dtype],
+        _ptr(workspace), nbytes, _stream(stream)), "kv8_attention")
+    return out

@@ -1,0 +1,140 @@
+"""Products of 8-bit integers with a scale per token and per output channel
+(the ``w8a8_*`` entry points of ``include/w4a16.h``).
+
+    wq, ws = w8a8_quantize(W)                  # once per layer, W [N, K]
+    y = w8a8_linear(x, wq, ws)                 # x [M, K] fp16/bf16, quantized per token
+
+or, for rows quantized once and used by several layers:
+
+    xq, xs = w8a8_quantize(x)
+    y = w8a8_gemm(xq, xs, wq, ws, dtype=torch.bfloat16)
+"""
+
+import contextlib
+
+import torch
+
+from . import _DT, _lib, _need, _ptr, _stream, _ws_cache
+
+_QDT = dict(_DT)
+_QDT[torch.float32] = 2
+
+
+def _empty(shape, dtype, device, stream=None):
+    """An output tensor of the stream that the kernel runs on (the caching
+    allocator reuses a block in the order of its own stream)."""
+    on = contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    with on:
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, dtypes, name, K=None):
+    """Checks a matrix of rows [..., K] whose last dimension is contiguous and
+    whose rows are evenly spaced; (rows, K, row stride in elements)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(map(str, dtypes)), t.dtype))
+    if t.dim() < 1 or t.shape[-1] == 0:
+        raise ValueError("%s has no columns" % name)
+    if K is not None and t.shape[-1] != K:
+        raise ValueError("%s last dim %d != K %d" % (name, t.shape[-1], K))
+    if t.dim() != 2 or t.stride(1) != 1:
+        t = _flat(t, name)
+    return t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _flat(t, name):
+    try:
+        t = t.view(-1, t.shape[-1])
+    except RuntimeError:
+        t = None
+    if t is None or t.stride(1) != 1:
+        raise ValueError("%s must have evenly spaced rows, contiguous within a row" % name)
+    return t
+
+
+def w8a8_workspace_bytes(M, N, K, linear=True):
+    """Bytes that w8a8_linear (or, linear=False, w8a8_gemm) needs at this shape."""
+    n = int(_lib.lib().w8a8_workspace_bytes(M, N, K, int(linear)))
+    if n < 0:
+        raise _lib.W4A16Error("w8a8_workspace_bytes: invalid shape M=%d N=%d K=%d" % (M, N, K))
+    return n
+
+
+def w8a8_quantize(x, stream=None):
+    """Rows of x [..., K] (fp16, bf16 or fp32) -> (codes int8 [..., K], scales
+    fp32 [...]): scale = max|row| / 127 (1 for a row of zeros)."""
+    M, K, stride = _rows(x, tuple(_QDT), "x")
+    codes = _empty(x.shape, torch.int8, x.device, stream)
+    scales = _empty(x.shape[:-1], torch.float32, x.device, stream)
+    _lib.check(_lib.lib().w8a8_quantize(_ptr(x), M, K, stride, _QDT[x.dtype], _ptr(codes),
+                                        _ptr(scales), _stream(stream)), "w8a8_quantize")
+    return codes, scales
+
+
+def _weights(wq, w_scale, bias, dtype):
+    _need(wq, torch.int8, "wq")
+    if wq.dim() != 2:
+        raise ValueError("wq must be [N, K]")
+    N, K = wq.shape
+    _need(w_scale, torch.float32, "w_scale", N)
+    if bias is not None:
+        _need(bias, dtype, "bias", N)
+    return N, K
+
+
+def _output(out, shape, dtype, device, stream):
+    if out is None:
+        return _empty(shape, dtype, device, stream)
+    n = 1
+    for d in shape:
+        n *= d
+    _need(out, dtype, "out", n)
+    return out
+
+
+def _space(workspace, need, device, stream):
+    if workspace is None and need > 0:
+        workspace = _ws_cache(device, need, stream)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, nbytes
+
+
+def w8a8_gemm(xq, x_scale, wq, w_scale, bias=None, dtype=torch.bfloat16, out=None,
+              workspace=None, use_workspace=True, stream=None):
+    """y = (xq @ wq^T) * x_scale * w_scale + bias in ``dtype`` (fp16 or bf16)
+    for codes xq [..., K], wq [N, K] from w8a8_quantize."""
+    if dtype not in _DT:
+        raise TypeError("dtype must be float16 or bfloat16")
+    N, K = _weights(wq, w_scale, bias, dtype)
+    _need(xq, torch.int8, "xq")
+    if xq.shape[-1] != K:
+        raise ValueError("xq last dim %d != K %d" % (xq.shape[-1], K))
+    M = xq.numel() // K
+    _need(x_scale, torch.float32, "x_scale", M)
+    out = _output(out, (*xq.shape[:-1], N), dtype, xq.device, stream)
+    nbytes = 0
+    if use_workspace:
+        need = max(0, int(_lib.lib().w8a8_workspace_bytes(M, N, K, 0)))
+        workspace, nbytes = _space(workspace, need, xq.device, stream)
+    else:
+        workspace = None
+    _lib.check(_lib.lib().w8a8_gemm(_ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias),
+                                    _ptr(out), M, N, K, _DT[dtype], _ptr(workspace), nbytes,
+                                    _stream(stream)), "w8a8_gemm")
+    return out
+
+
+def w8a8_linear(x, wq, w_scale, bias=None, out=None, workspace=None, stream=None):
+    """y = x @ (wq * w_scale)^T + bias for x [..., K] fp16/bf16, quantized per
+    row on the way (w8a8_quantize and w8a8_gemm in one call)."""
+    M, K, stride = _rows(x, tuple(_DT), "x", wq.shape[-1])
+    N, _ = _weights(wq, w_scale, bias, x.dtype)
+    out = _output(out, (*x.shape[:-1], N), x.dtype, x.device, stream)
+    need = max(0, int(_lib.lib().w8a8_workspace_bytes(M, N, K, 1)))
+    workspace, nbytes = _space(workspace, need, x.device, stream)
+    _lib.check(_lib.lib().w8a8_linear(_ptr(x), stride, _ptr(wq), _ptr(w_scale), _ptr(bias),
+                                      _ptr(out), M, N, K, _DT[x.dtype], _ptr(workspace), nbytes,
+                                      _stream(stream)), "w8a8_linear")
+    return out

@@ -66,7 +66,8 @@ typedef enum {
   W4A16_ERR_HOST = 7           /* host-side failure (host memory allocation)      */
 } w4a16_status_t;
 
-typedef enum { W4A16_F16 = 0, W4A16_BF16 = 1 } w4a16_dtype_t;
+/* W4A16_F32 is taken by w8a8_quantize alone. */
+typedef enum { W4A16_F16 = 0, W4A16_BF16 = 1, W4A16_F32 = 2 } w4a16_dtype_t;
 
 /* Which array w4a16_repacked_bytes sizes. */
 typedef enum { W4A16_CODES = 0, W4A16_SCALES = 1, W4A16_ZEROS = 2 } w4a16_array_t;
@@ -479,6 +480,158 @@ int nf4_gemm_repacked_plan(int64_t M, int64_t N, int64_t K, int32_t blocksize, i
 int nf4_dequant(const uint8_t* qweight, const uint8_t* absmax_q, const float* absmax_scale,
                 int64_t N, int64_t K, int32_t blocksize, int32_t dtype, void* w_out,
                 void* stream);
+
+/* ------------------------------------------------- 8-bit integer product --- */
+
+/*
+ * Both operands in 8-bit integers, one fp32 scale per token (row of x) and
+ * per output channel (row of w), for calls that the 16-bit matrix rate would
+ * bound (prompts, large batches):
+ *   y[m, n] = round_dtype(fp32(sum_k cx[m, k] cw[n, k]) * (sx[m] * sw[n]) + b[n]).
+ * Codes are int8 in [-127, 127].  The sum over k is exact in int32, so a
+ * result does not depend on any split of K.  Weights and codes are row-major
+ * as they are: no repacking.
+ * Constraints: M >= 1, K % 16 == 0, N % 8 == 0 (W4A16_ERR_INVALID_ARG);
+ * M <= 2^21, N <= 2^24, K <= 2^17, M * N <= 2^36 (W4A16_ERR_UNSUPPORTED).
+ *
+ * w8a8_quantize: rows of x [M, K], row stride x_stride elements (>= K, a
+ * multiple of 8), in fp16, bf16 or fp32 -> codes int8 [M, K] and scales fp32
+ * [M], for activations (on the fly) and weights (once) alike:
+ *   s = fp32(max|x| * fp32(1/127)) (1 where that is 0),
+ *   c = clip(rint(x / s), -127, 127), in fp32, rint = half to even.
+ * A row with an infinity or a NaN has the scale NaN (and y NaN).
+ */
+int w8a8_quantize(const void* x, int64_t M, int64_t K, int64_t x_stride, int32_t dtype,
+                  int8_t* codes, float* scales, void* stream);
+
+/*
+ * Workspace bytes of w8a8_gemm (linear = 0) or w8a8_linear (linear = 1) at
+ * this shape; -1 on bad input.  Calls that overlap in time must not share a
+ * workspace; its contents need not be initialized.
+ */
+int64_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t linear);
+
+/*
+ * The product of quantized rows.
+ *   xq int8 [M, K], x_scale fp32 [M]; wq int8 [N, K], w_scale fp32 [N];
+ *   bias [N] in dtype or NULL; out [M, N] in dtype.
+ *   workspace: optional, as for w4a16_gemm.
+ * Async.  Bitwise reproducible.
+ */
+int w8a8_gemm(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+              const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t dtype,
+              void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * w8a8_quantize of x (fp16 or bf16, row stride x_stride) and w8a8_gemm in one
+ * call: bitwise the same output.  The codes go to the workspace, which is
+ * required where w8a8_workspace_bytes(M, N, K, 1) is not 0
+ * (W4A16_ERR_WORKSPACE when NULL or smaller).
+ */
+int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* w_scale,
+                const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t dtype,
+                void* workspace, int64_t workspace_bytes, void* stream);
+
+/* -------------------------------------------------- paged cache in 8 bits --- */
+
+/*
+ * Keys and values of attention in pages of T = page_size tokens (16, 32, 64
+ * or 128) of every kv head, D channels (64 or 128) in 8 bits with one fp32
+ * scale per (page, kv head):
+ *   k_cache uint8 [num_pages][Hkv][T][D]
+ *   v_cache uint8 [num_pages][Hkv][T / 16][D][16]  (16 tokens innermost)
+ *   k_scale, v_scale fp32 [num_pages][Hkv]
+ * a code c stands for (c - 128) * scale, c - 128 in [-127, 127].
+ *
+ * Sequences: token p of sequence b is row p % T of page
+ * page_table[b][p / T] (int32 [B][max_pages]); seq_lens[b] (int32 [B]) counts
+ * its tokens, the new ones included.  The new tokens (rows of k, v, q) of
+ * sequence b are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]),
+ * at positions seq_lens[b] - n .. seq_lens[b] - 1, n their count (0 is
+ * legal); cu_seqlens NULL: one new token for each sequence, in order (tokens
+ * == B).  max_new is an upper bound of n (<= tokens; 1 with cu_seqlens NULL);
+ * rows past it in a sequence are not processed.  Tables, lengths and offsets
+ * stay on the device: entries out of range are brought into range, so they
+ * give unspecified values but no access outside the arrays; table entries
+ * past a sequence's last page are not used.  A token at a negative position
+ * (n > seq_lens[b]) is not stored and sees nothing.
+ * Rows of q, k, v and out are [heads][D] with a row stride in elements (a
+ * multiple of 8, at least heads * D), so slices of a fused projection can be
+ * passed as they are.
+ * Limits (W4A16_ERR_UNSUPPORTED): tokens <= 2^24, B <= 2^20, H <= 1024,
+ * max_pages * T <= 2^30, num_pages <= 2^30, grids below 2^31 workgroups.
+ * tokens, B or max_new of 0 launches nothing.
+ */
+
+/*
+ * Appends k and v [tokens][Hkv][D] (dtype fp16 or bf16) to the cache,
+ * rotating the keys by their positions on the way, and writes the rotated
+ * queries q [tokens][H][D] -> q_out (both NULL: no queries; q_out == q is
+ * legal).
+ *   cos, sin  fp32 [rope_rows][rope_dim / 2] (both NULL: no rotation), rows
+ *             by position; rope_dim <= D, rope_dim % 16 == 0, channels past it
+ *             pass through.  Pair i, (a, b) -> (a cos - b sin, b cos + a sin)
+ *             with fp32 products and sums, each rounded once, is channels
+ *             (i, i + rope_dim / 2), or (2i, 2i + 1) when `interleaved`.
+ * Keys are quantized from fp32 without rounding to 16 bits first.  Per (page,
+ * kv head), for keys and values each: s' = max(s, fp32(max|new rows| *
+ * fp32(1/127))), with s = 0 if the call writes the page's row 0 and its
+ * present scale otherwise; if s' > s the page's older rows become
+ * rint(c * fp32(s / s')) (c signed); new rows are clip(rint(x / s'), -127,
+ * 127) (0 where s' is 0).  Rows past the new ones keep their bytes.  A new row
+ * with an infinity or a NaN makes the page's scale for that head NaN.
+ * No two sequences of a call may append to the same page.  Async; appending
+ * the same rows again changes nothing.
+ */
+int kv8_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+               int64_t k_stride, const void* v, int64_t v_stride, uint8_t* k_cache,
+               uint8_t* v_cache, float* k_scale, float* v_scale, int64_t num_pages,
+               int32_t page_size, const int32_t* page_table, int64_t max_pages,
+               const int32_t* seq_lens, const int32_t* cu_seqlens, const float* cos,
+               const float* sin, int64_t rope_rows, int32_t rope_dim, int32_t interleaved,
+               int64_t tokens, int64_t B, int64_t max_new, int32_t H, int32_t Hkv, int32_t D,
+               int32_t dtype, void* stream);
+
+/*
+ * Reads pages back: k_out, v_out [n][Hkv][T][D] in dtype = round(fp32((c -
+ * 128) * scale)) of pages[0 .. n - 1] (int32, device).  Async.
+ */
+int kv8_dequant(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                const float* v_scale, int64_t num_pages, int32_t page_size, int32_t Hkv,
+                int32_t D, const int32_t* pages, int64_t n, int32_t dtype, void* k_out,
+                void* v_out, void* stream);
+
+/*
+ * Workspace bytes of kv8_attention for these sizes (the partial results of
+ * keys split over workgroups; 0 where none is split); -1 on bad input.
+ */
+int64_t kv8_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t max_new, int64_t max_len,
+                                      int32_t H, int32_t Hkv, int32_t D);
+
+/*
+ * Attention of the new tokens' queries over their sequences' cached tokens
+ * (which kv8_append has written, the new ones among them):
+ *   out[t][h] = sum_l softmax_l(scale q[t][h] . K[l]) V[l],  kv head h / (H / Hkv),
+ * over the visible l: every cached token up to the query's own position
+ * (causal != 0), or all seq_lens[b] of them.  A query that sees nothing gives
+ * 0 (and lse -inf).  Scores, the softmax's maximum and sum and the output
+ * are held in fp32; probabilities enter the second product as fp16, queries
+ * as fp16 (bf16 rows after an exact power of two); one rounding to dtype.
+ *   lse       fp32 [tokens][H] or NULL: log(sum exp(scale q . K)), natural.
+ *   max_len   an upper bound of the seq_lens (<= max_pages * T), by which the
+ *             split of the keys is planned; longer sequences are cut to
+ *             the planned units.
+ *   workspace required where kv8_attention_workspace_bytes is not 0
+ *             (W4A16_ERR_WORKSPACE when NULL or smaller).
+ * Async.  Bitwise reproducible (splits are joined in order).
+ */
+int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                  const float* k_scale, const float* v_scale, int64_t num_pages,
+                  int32_t page_size, const int32_t* page_table, int64_t max_pages,
+                  const int32_t* seq_lens, const int32_t* cu_seqlens, float scale, int32_t causal,
+                  void* out, int64_t out_stride, float* lse, int64_t tokens, int64_t B,
+                  int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
+                  int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
