@@ -103,6 +103,174 @@ hipError_t launch_quantize(const void* x, int64_t M, int64_t K, int64_t stride, 
 }
 
 // ---------------------------------------------------------------- product ---
+// 16 bytes per lane from a buffer straight into LDS: lane l's data lands at
+// lds + 16 l (the LDS base is wave-uniform).
+__device__ __forceinline__ void dma16(rsrc_t r, uint8_t* lds, uint32_t voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
+}
+
+// Tile shape: WM x WN waves, each MT x NT products of 32 x 32.
+template <int MT_, int NT_, int WM_, int WN_, int NS_>
+struct Tile {
+  static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr int WAVES = WM * WN, BM = 32 * MT * WM, BN = 32 * NT * WN;
+  static constexpr int STAGE = (BM + BN) * 64;           // bytes of one K step of 64
+  static constexpr int LOADS = (BM + BN) / 16 / WAVES;   // 1 KB loads per wave and step
+  static_assert((BM + BN) / 16 % WAVES == 0 && NS >= 4, "whole loads per wave");
+};
+
+// One workgroup per BM x BN tile of y on v_mfma_i32_32x32x32_i8, the rows of
+// w as the first operand (so that a lane's 4 consecutive results are 4
+// channels of one token).
+//
+//  * K goes by in steps of 64 codes.  A step's rows of w and x come straight
+//    into LDS (64-byte rows; the 16-byte chunk q of row r at position
+//    q ^ (r >> 1 & 3), so that 8 lanes reading one chunk of 8 rows meet all
+//    banks), NS steps deep: the loads of step t + NS - 1 go out during step t.
+//  * A step is two halves of 32 codes.  The operands of a half are read while
+//    the products of the half before run, across the step's boundary too: the
+//    wait and the barrier for step t + 1 stand in the middle of step t.
+//  * The results pass through LDS into whole 64 NT-byte rows of y.
+template <int DT, class TL>
+__global__ void __launch_bounds__(64 * TL::WAVES)
+w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
+                 const int8_t* __restrict__ wq, const float* __restrict__ sw,
+                 const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
+                 int K, int mb, int nb, int per_xcd) {
+  constexpr int MT = TL::MT, NT = TL::NT, NS = TL::NS, L = TL::LOADS;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NS * TL::STAGE];
+  // ---- tile of this workgroup: workgroups go to the 8 XCDs in turn, so each
+  // XCD takes a contiguous run of tiles, ordered in bands of 8 row blocks
+  const int at = (int)(blockIdx.x & 7) * per_xcd + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per_xcd || at >= mb * nb) return;
+  const int band = at / (8 * nb), in_band = at % (8 * nb);
+  const int bh = min(8, mb - band * 8);
+  const int row0 = (band * 8 + in_band % bh) * TL::BM, col0 = in_band / bh * TL::BN;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / TL::WN, wn = wave % TL::WN;
+  const int KT = (K + 63) >> 6;
+  const rsrc_t rw = make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(TL::BN, N - col0) * (uint32_t)K);
+  const rsrc_t rx = make_rsrc(xq + (size_t)row0 * K, (uint32_t)min(TL::BM, M - row0) * (uint32_t)K);
+
+  // load i of this wave fills the LDS block WAVES i + wave (16 rows); blocks
+  // below BN / 16 are rows of w
+  const int lrow = lane >> 2, lchunk = (lane & 3) ^ ((lane >> 3) & 3);
+  const uint32_t lane_off = (uint32_t)lrow * (uint32_t)K + 16u * lchunk;
+  // chunks of the last step that lie past K
+  const uint32_t tail = 64 * (KT - 1) + 16 * lchunk >= K ? kOutOfRange : 0u;
+  auto load = [&](int t, int i) {
+    const int blk = TL::WAVES * i + wave;
+    const bool is_w = blk < TL::BN / 16;
+    const uint32_t row = 16u * (uint32_t)(is_w ? blk : blk - TL::BN / 16);
+    uint32_t off = lane_off + row * (uint32_t)K;
+    off |= t < KT - 1 ? 0u : t == KT - 1 ? tail : kOutOfRange;
+    dma16(is_w ? rw : rx, lds + (t % NS) * TL::STAGE + blk * 1024, off, t * 64);
+  };
+
+  const int r = lane & 31, h = lane >> 5;
+  const uint32_t swz = (r >> 1) & 3;
+  const uint32_t woff = (uint32_t)(wn * NT * 32 + r) * 64, xoff = (uint32_t)(TL::BN + wm * MT * 32 + r) * 64;
+  i32x4_t fw[2][NT], fx[2][MT];
+  auto read = [&](int t, int half, i32x4_t (&w)[NT], i32x4_t (&x)[MT]) {
+    const uint8_t* st = lds + (t % NS) * TL::STAGE + (((2 * half + h) ^ swz) << 4);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) w[i] = *(const i32x4_t*)(st + woff + i * 2048);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) x[i] = *(const i32x4_t*)(st + xoff + i * 2048);
+  };
+  i32x16_t acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = i32x16_t{};
+  auto products = [&](const i32x4_t (&w)[NT], const i32x4_t (&x)[MT]) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], x[j], acc[i][j], 0, 0, 0);
+  };
+
+#pragma unroll
+  for (int t = 0; t < NS - 1; ++t)
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(t, i);
+  // step 0 is complete: the loads of NS - 2 later steps may be pending
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 2) * L) : "memory");
+  read(0, 0, fw[0], fx[0]);
+  for (int t = 0; t < KT; ++t) {
+    read(t, 1, fw[1], fx[1]);
+    products(fw[0], fx[0]);
+#pragma unroll
+    for (int k = 0; k < MT * NT; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one product
+      if (k < (MT + NT + 1) / 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // two reads
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // step t + 1 is complete in LDS, and every wave is done with step t - 1
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 3) * L) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    read(t + 1, 0, fw[0], fx[0]);
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(t + NS - 1, i);
+    products(fw[1], fx[1]);
+    // the reads first: a load into LDS may not pass a read before it
+    constexpr int RD = (MT + NT + 1) / 2, PER = (L + MT * NT - RD - 1) / (MT * NT - RD);
+#pragma unroll
+    for (int k = 0; k < MT * NT; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (k < RD) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      else __builtin_amdgcn_sched_group_barrier(0x020, PER, 0);  // loads
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // the loads past the last step have written their zeros
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // ---- results: register i of product (nt, mt) is channel 8 (i >> 2) + 4 h +
+  // (i & 3) of its 32, token lane & 31; one 32-token block of the wave at a time
+  constexpr int ROW = NT * 64 + 16;  // bytes of a token's row in LDS
+  static_assert(TL::WAVES * 32 * ROW <= NS * TL::STAGE, "the results fit");
+  uint8_t* mine = lds + wave * 32 * ROW;
+  const int wcol = col0 + wn * NT * 32;
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int mrow = row0 + (wm * MT + j) * 32;
+    const float s = mrow + r < M ? sx[mrow + r] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int n = wcol + i * 32 + 8 * g + 4 * h;
+        float4_t t = {0, 0, 0, 0};
+        u32x2_t b = {0, 0};
+        if (n < N) {
+          t = *(const float4_t*)(sw + n);
+          if (bias) b = *(const u32x2_t*)(bias + n);
+        }
+        uint16_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y[e] = round16<DT>((float)acc[i][j][4 * g + e] * (s * t[e]) +
+                             widen16<DT>((uint16_t)(b[e >> 1] >> (16 * (e & 1)))));
+        const u32x2_t v = {(uint32_t)y[0] | (uint32_t)y[1] << 16, (uint32_t)y[2] | (uint32_t)y[3] << 16};
+        *(u32x2_t*)(mine + r * ROW + i * 64 + 16 * g + 8 * h) = v;
+      }
+    constexpr int LR = NT * 4;  // lanes per row
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int k = 0; k < 32 / (64 / LR); ++k) {
+      const int tr = k * (64 / LR) + lane / LR, c = (lane % LR) * 8;
+      const u32x4_t v = *(const u32x4_t*)(mine + tr * ROW + c * 2);
+      if (mrow + tr < M && wcol + c < N) *(u32x4_t*)(out + (size_t)(mrow + tr) * N + wcol + c) = v;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 // One wave per 32 x 32 tile of y on v_mfma_i32_32x32x32_i8, operands straight
 // from memory: lane l holds 16 codes of row l & 31 at inputs 16 (l >> 5) of a
 // step; rows past the end and inputs past K read 0.
@@ -136,17 +304,37 @@ w8a8_gemm_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   }
 }
 
+typedef Tile<4, 4, 2, 2, 5> T256;
+typedef Tile<2, 2, 2, 2, 4> T128;
+
+template <int DT, class TL>
+void launch_tile(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                 const void* bias, void* out, int64_t M, int64_t N, int64_t K, hipStream_t st) {
+  const int mb = (int)ceil_div(M, TL::BM), nb = (int)ceil_div(N, TL::BN);
+  const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
+  launch_timed(w8a8_tile_kernel<DT, TL>, dim3((unsigned)per_xcd * 8), dim3(64 * TL::WAVES), 0, st,
+               xq, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K, mb,
+               nb, per_xcd);
+}
+
+template <int DT>
+hipError_t launch_gemm_dt(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                          const void* bias, void* out, int64_t M, int64_t N, int64_t K,
+                          hipStream_t st) {
+  if (M > 256) launch_tile<DT, T256>(xq, sx, wq, sw, bias, out, M, N, K, st);
+  else if (M > 64) launch_tile<DT, T128>(xq, sx, wq, sw, bias, out, M, N, K, st);
+  else
+    launch_timed(w8a8_gemm_kernel<DT>, dim3((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64)),
+                 dim3(256), 0, st, xq, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M,
+                 (int)N, (int)K);
+  return hipGetLastError();
+}
+
 hipError_t launch_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                        const void* bias, void* out, int64_t M, int64_t N, int64_t K, int dtype,
                        hipStream_t st) {
-  const dim3 g((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64)), b(256);
-  if (dtype == DT_F16)
-    launch_timed(w8a8_gemm_kernel<DT_F16>, g, b, 0, st, xq, sx, wq, sw, (const uint16_t*)bias,
-                 (uint16_t*)out, (int)M, (int)N, (int)K);
-  else
-    launch_timed(w8a8_gemm_kernel<DT_BF16>, g, b, 0, st, xq, sx, wq, sw, (const uint16_t*)bias,
-                 (uint16_t*)out, (int)M, (int)N, (int)K);
-  return hipGetLastError();
+  return (dtype == DT_F16 ? launch_gemm_dt<DT_F16> : launch_gemm_dt<DT_BF16>)(
+      xq, sx, wq, sw, bias, out, M, N, K, st);
 }
 
 // --------------------------------------------------------------- checking ---
