@@ -6,7 +6,9 @@
 //
 // The sum is exact in int32 (|c| <= 127 and K <= 2^17), so it does not depend
 // on any split of K.
+#include <algorithm>
 #include <cstdio>
+#include <type_traits>
 
 #include "abi.h"
 #include "launch.h"
@@ -110,6 +112,35 @@ __device__ __forceinline__ void dma16(rsrc_t r, uint8_t* lds, uint32_t voff, int
       r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
 }
 
+// Two fp32 values rounded to 16 bits, in one register.
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (DT == DT_F16) {
+    const half2_t v = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  } else {
+    const bf16x2_t v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+}
+
+// One result in fp32: the sum times the two scales, plus the bias.  Every
+// kernel here forms it by these operations, so that the choice of a kernel
+// does not show in the result.
+__device__ __forceinline__ float result(int acc, float s, float t, float bias) {
+  return __builtin_fmaf((float)acc, s * t, bias);
+}
+
+// Results 4 g .. 4 g + 3 of a product: 4 channels of one token, in 16 bits.
+template <int DT>
+__device__ __forceinline__ u32x2_t results4(const i32x16_t& acc, int g, float s, float4_t t,
+                                            float4_t bias) {
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = result(acc[4 * g + e], s, t[e], bias[e]);
+  return u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
+}
+
 // Tile shape: WM x WN waves, each MT x NT products of 32 x 32.
 template <int MT_, int NT_, int WM_, int WN_, int NS_>
 struct Tile {
@@ -126,7 +157,7 @@ struct Tile {
 //
 //  * K goes by in steps of 64 codes.  A step's rows of w and x come straight
 //    into LDS (64-byte rows; the 16-byte chunk q of row r at position
-//    q ^ (r >> 1 & 3), so that 8 lanes reading one chunk of 8 rows meet all
+//    q ^ (r >> 2 & 3), so that 16 lanes reading one chunk of 16 rows meet all
 //    banks), NS steps deep: the loads of step t + NS - 1 go out during step t.
 //  * A step is two halves of 32 codes.  The operands of a half are read while
 //    the products of the half before run, across the step's boundary too: the
@@ -157,7 +188,7 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 
   // load i of this wave fills the LDS block WAVES i + wave (16 rows); blocks
   // below BN / 16 are rows of w
-  const int lrow = lane >> 2, lchunk = (lane & 3) ^ ((lane >> 3) & 3);
+  const int lrow = lane >> 2, lchunk = (lane & 3) ^ ((lane >> 4) & 3);
   const uint32_t lane_off = (uint32_t)lrow * (uint32_t)K + 16u * lchunk;
   // chunks of the last step that lie past K
   const uint32_t tail = 64 * (KT - 1) + 16 * lchunk >= K ? kOutOfRange : 0u;
@@ -171,7 +202,7 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   };
 
   const int r = lane & 31, h = lane >> 5;
-  const uint32_t swz = (r >> 1) & 3;
+  const uint32_t swz = (r >> 2) & 3;
   const uint32_t woff = (uint32_t)(wn * NT * 32 + r) * 64, xoff = (uint32_t)(TL::BN + wm * MT * 32 + r) * 64;
   i32x4_t fw[2][NT], fx[2][MT];
   auto read = [&](int t, int half, i32x4_t (&w)[NT], i32x4_t (&x)[MT]) {
@@ -245,19 +276,17 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int n = wcol + i * 32 + 8 * g + 4 * h;
-        float4_t t = {0, 0, 0, 0};
-        u32x2_t b = {0, 0};
+        float4_t t = {0, 0, 0, 0}, b = {0, 0, 0, 0};
         if (n < N) {
           t = *(const float4_t*)(sw + n);
-          if (bias) b = *(const u32x2_t*)(bias + n);
-        }
-        uint16_t y[4];
+          if (bias) {
+            const u32x2_t w = *(const u32x2_t*)(bias + n);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y[e] = round16<DT>((float)acc[i][j][4 * g + e] * (s * t[e]) +
-                             widen16<DT>((uint16_t)(b[e >> 1] >> (16 * (e & 1)))));
-        const u32x2_t v = {(uint32_t)y[0] | (uint32_t)y[1] << 16, (uint32_t)y[2] | (uint32_t)y[3] << 16};
-        *(u32x2_t*)(mine + r * ROW + i * 64 + 16 * g + 8 * h) = v;
+            for (int e = 0; e < 4; ++e)
+              b[e] = widen16<DT>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+          }
+        }
+        *(u32x2_t*)(mine + r * ROW + i * 64 + 16 * g + 8 * h) = results4<DT>(acc[i][j], g, s, t, b);
       }
     constexpr int LR = NT * 4;  // lanes per row
     __builtin_amdgcn_wave_barrier();
@@ -268,6 +297,218 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
       if (mrow + tr < M && wcol + c < N) *(u32x4_t*)(out + (size_t)(mrow + tr) * N + wcol + c) = v;
     }
     __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// The same product for many tokens: workgroups stay and take 256 x 256 tiles
+// in turn, 4 waves of 4 x 4 products.  K goes by in steps of 128 codes (whole
+// 128-byte lines of w and x), four quarters of 32 each:
+//
+//  * The rows of step t + 2 are loaded into registers while step t runs, each
+//    register right after its part of step t + 1 went from it to LDS, so a load
+//    has a whole step to arrive; LDS holds two steps (64 KB each; chunk q of row
+//    r at position q ^ (r >> 1 & 7): 16 lanes reading one chunk of 16 rows meet
+//    all banks).  One barrier per step, before its last quarter.
+//  * The operands of a quarter are read while the products of the quarter
+//    before run.  Steps go on across tiles: a tile's first rows and operands
+//    arrive during the last step and the results of the tile before.
+//  * The results pass through LDS of their own into whole 128-byte pieces of
+//    y's rows; the tile's scales and bias wait there since its first step.
+constexpr int kWideStage = 512 * 128, kWideTurn = 2 * kWideStage, kWideScales = kWideTurn + 4 * 4096;
+constexpr int kWideLds = kWideScales + 256 * 12;  // x's scales, w's, the bias as fp32
+
+template <int DT>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
+                 const int8_t* __restrict__ wq, const float* __restrict__ sw,
+                 const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
+                 int K, int mb, int nb, int per_xcd) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWideLds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int KT = (K + 127) >> 7;
+
+  // ---- tiles of this workgroup: each XCD has a contiguous run of them, in
+  // bands of 8 row blocks; its workgroups take them in turn
+  const int run0 = (int)(blockIdx.x & 7) * per_xcd;
+  const int run1 = min(run0 + per_xcd, mb * nb);
+  const int every = (int)(gridDim.x >> 3);
+  const int first = run0 + (int)(blockIdx.x >> 3);
+  if (first >= run1) return;
+  auto tile_at = [&](int at, int& row0, int& col0) {
+    const int band = at / (8 * nb), in_band = at % (8 * nb);
+    const int bh = min(8, mb - band * 8);
+    row0 = (band * 8 + in_band % bh) * 256;
+    col0 = in_band / bh * 256;
+  };
+
+  // ---- loads: instruction i of a step fetches 8 rows x 128 bytes, i < 8 rows
+  // of w and i >= 8 rows of x, of rows 64 wave + 8 (i & 7) of the tile
+  const int lrow = lane >> 3, lchunk = lane & 7;
+  const uint32_t lane_off = (uint32_t)(64 * wave + lrow) * (uint32_t)K + 16u * lchunk;
+  const uint32_t tail = 128 * (KT - 1) + 16 * lchunk >= K ? kOutOfRange : 0u;
+  const uint32_t lane_lds = (uint32_t)(64 * wave + lrow) * 128 + 16u * (lchunk ^ ((lrow >> 1) & 3));
+  int lat = first, lt = 0;  // the step that is loaded next
+  rsrc_t rw, rx;
+  auto aim = [&]() {
+    int row0 = 0, col0 = 0;
+    const bool any = lat < run1;
+    if (any) tile_at(lat, row0, col0);
+    rw = make_rsrc(wq + (size_t)col0 * K, any ? (uint32_t)min(256, N - col0) * (uint32_t)K : 0u);
+    rx = make_rsrc(xq + (size_t)row0 * K, any ? (uint32_t)min(256, M - row0) * (uint32_t)K : 0u);
+  };
+  aim();
+  i32x4_t held[16];
+  auto load = [&](int i) {
+    const uint32_t off = (lane_off + (uint32_t)(8 * (i & 7)) * (uint32_t)K) | (lt == KT - 1 ? tail : 0u);
+    held[i] = __builtin_bit_cast(i32x4_t, bld128(i < 8 ? rw : rx, off, lt * 128));
+  };
+  auto loaded = [&]() {  // every load of a step is out
+    if (++lt == KT) {
+      lt = 0;
+      lat += every;
+      aim();
+    }
+  };
+  // row 64 wave + 8 i + lrow: (row >> 1) & 7 is ((lrow >> 1) & 3) + 4 (i & 1)
+  auto store = [&](int slot, int i) {
+    *(i32x4_t*)(lds + slot * kWideStage + (i < 8 ? 0 : 32768) + (i & 7) * 1024 +
+                (lane_lds ^ ((i & 1) << 6))) = held[i];
+  };
+
+  const int r = lane & 31, h = lane >> 5;
+  i32x4_t fw[2][4], fx[2][4];
+  auto read = [&](int slot, int quarter, i32x4_t (&w)[4], i32x4_t (&x)[4]) {
+    const uint8_t* st = lds + slot * kWideStage + (((2 * quarter + h) ^ ((r >> 1) & 7)) << 4) + r * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *(const i32x4_t*)(st + wn * 16384 + i * 4096);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *(const i32x4_t*)(st + 32768 + wm * 16384 + i * 4096);
+  };
+  i32x16_t acc[4][4];
+  auto products = [&](const i32x4_t (&w)[4], const i32x4_t (&x)[4], bool anew) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], x[j], anew ? i32x16_t{} : acc[i][j],
+                                                          0, 0, 0);
+  };
+  // one quarter: 16 products, and between them 8 reads, `n` stores from
+  // registers each followed by its load
+  auto order = [&](auto n) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (k < 4) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      else if (2 * (k - 4) < 2 * decltype(n)::value && k - 4 < decltype(n)::value) {
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // ---- the first step goes to LDS, the second to registers
+#pragma unroll
+  for (int i = 0; i < 16; ++i) load(i);
+  loaded();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) store(0, i);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) load(i);
+  loaded();
+  __syncthreads();
+  read(0, 0, fw[0], fx[0]);
+  int slot = 0;
+  float sx_v = 0.0f, sw_v = 0.0f, bias_v = 0.0f;
+  float* scales = (float*)(lds + kWideScales);
+  auto step = [&](auto anew) {
+    read(slot, 1, fw[1], fx[1]);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) store(slot ^ 1, i), load(i);
+    products(fw[0], fx[0], decltype(anew)::value);
+    order(std::integral_constant<int, 6>{});
+    read(slot, 2, fw[0], fx[0]);
+#pragma unroll
+    for (int i = 6; i < 12; ++i) store(slot ^ 1, i), load(i);
+    products(fw[1], fx[1], false);
+    order(std::integral_constant<int, 6>{});
+    read(slot, 3, fw[1], fx[1]);
+#pragma unroll
+    for (int i = 12; i < 16; ++i) store(slot ^ 1, i), load(i);
+    products(fw[0], fx[0], false);
+    order(std::integral_constant<int, 4>{});
+    loaded();
+    if (decltype(anew)::value) {
+      scales[tid] = sx_v;
+      scales[256 + tid] = sw_v;
+      scales[512 + tid] = bias_v;
+    }
+    // the next step is whole in LDS, and nobody reads this one any more
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    slot ^= 1;
+    read(slot, 0, fw[0], fx[0]);
+    products(fw[1], fx[1], false);
+    order(std::integral_constant<int, 0>{});
+  };
+  uint8_t* mine = lds + kWideTurn + wave * 4096;
+  for (int at = first; at < run1; at += every) {
+    int row0, col0;
+    tile_at(at, row0, col0);
+    sx_v = row0 + tid < M ? sx[row0 + tid] : 0.0f;
+    sw_v = col0 + tid < N ? sw[col0 + tid] : 0.0f;
+    bias_v = bias && col0 + tid < N ? widen16<DT>(bias[col0 + tid]) : 0.0f;
+    step(std::true_type{});
+    for (int t = 1; t < KT; ++t) step(std::false_type{});
+    // the sums stay in accumulation registers until their block's turn
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
+
+    // ---- results: register e of product (i, j) is channel 8 (e >> 2) + 4 h +
+    // (e & 3) of its 32, token lane & 31; blocks of 32 tokens x 64 channels, the
+    // 16-byte chunk c of token r at position c ^ (r & 7)
+    const int wcol = col0 + wn * 128;
+    // (hidden from the compiler, which would keep every address of this part
+    // in registers all through the steps, and spill)
+    int at_lane = lane;
+    asm volatile("" : "+v"(at_lane));
+    const int r = at_lane & 31, h = at_lane >> 5;
+#pragma unroll
+    for (int i0 = 0; i0 < 4; i0 += 2) {
+      const float* sn = scales + 256 + wn * 128 + i0 * 32 + 4 * h;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int mrow = row0 + (wm * 4 + j) * 32;
+        const float s = scales[(wm * 4 + j) * 32 + r];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            // (the scales are read again for each block of tokens: held, they
+            // would cost the registers that the next tile's rows wait in)
+            const float4_t t = *(const float4_t*)(sn + i * 32 + 8 * g);
+            const float4_t b = *(const float4_t*)(sn + 256 + i * 32 + 8 * g);
+            *(u32x2_t*)(mine + r * 128 + (((i * 4 + g) ^ (r & 7)) << 4) + 8 * h) =
+                results4<DT>(acc[i0 + i][j], g, s, t, b);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_wave_barrier();
+        const int c = at_lane & 7, n = wcol + i0 * 32 + c * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tr = k * 8 + (at_lane >> 3);
+          const u32x4_t v = *(const u32x4_t*)(mine + tr * 128 + ((c ^ (tr & 7)) << 4));
+          if (mrow + tr < M && n < N)
+            *(u32x4_t*)(out + (size_t)(mrow + tr) * N + n) = v;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
   }
 }
 
@@ -300,7 +541,7 @@ w8a8_gemm_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int row = row0 + (i & 3) + 4 * h + 8 * (i >> 2);
-    if (row < M) out[(size_t)row * N + col] = round16<DT>((float)acc[i] * (sx[row] * t) + b);
+    if (row < M) out[(size_t)row * N + col] = round16<DT>(result(acc[i], sx[row], t, b));
   }
 }
 
@@ -321,7 +562,13 @@ template <int DT>
 hipError_t launch_gemm_dt(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                           const void* bias, void* out, int64_t M, int64_t N, int64_t K,
                           hipStream_t st) {
-  if (M > 256) launch_tile<DT, T256>(xq, sx, wq, sw, bias, out, M, N, K, st);
+  if (M > 256) {
+    const int mb = (int)ceil_div(M, 256), nb = (int)ceil_div(N, 256);
+    const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
+    launch_timed(w8a8_wide_kernel<DT>, dim3((unsigned)std::min(256, per_xcd * 8)), dim3(256), 0, st,
+                 xq, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K, mb,
+                 nb, per_xcd);
+  }
   else if (M > 64) launch_tile<DT, T128>(xq, sx, wq, sw, bias, out, M, N, K, st);
   else
     launch_timed(w8a8_gemm_kernel<DT>, dim3((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64)),
