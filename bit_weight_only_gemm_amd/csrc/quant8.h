@@ -32,6 +32,30 @@ __device__ __forceinline__ int code_of(float x, float s) {
   return (int)fminf(fmaxf(rintf(x / s), -127.0f), 127.0f);
 }
 
+// The codes of 8 values, code_of's without its divisions: n = rint(x fp32(1/s))
+// is the same unless x / s lies within 2^-12 or so of a half-integer, and
+// fma(-n, s, x) / s says how far it is from n to far better than that.  Where
+// one of the 8 is that near (or s too small for its reciprocal), all are
+// divided.
+struct Codes8 {
+  float s, inv, near;
+  __device__ __forceinline__ explicit Codes8(float scale)
+      : s(scale), inv(1.0f / scale), near(scale > 1e-30f ? 0.4995f * scale : -1.0f) {}
+  __device__ __forceinline__ void operator()(const float (&x)[8], int (&c)[8]) const {
+    float far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float n = rintf(x[i] * inv);
+      far = fmaxf(far, fabsf(__builtin_fmaf(-n, s, x[i])));
+      c[i] = (int)n;
+    }
+    if (!(far < near)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = code_of(x[i], s);
+    }
+  }
+};
+
 // Largest magnitude over a group of lanes (offsets below N, a power of two).
 template <int N>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {

@@ -39,11 +39,12 @@ __device__ __forceinline__ void load8(const void* x, int64_t i, float (&f)[8]) {
   }
 }
 
-__device__ __forceinline__ u32x2_t codes8(const float (&f)[8], float s) {
+__device__ __forceinline__ u32x2_t codes8(const float (&f)[8], const Codes8& q) {
+  int c[8];
+  q(f, c);
   u32x2_t r = {0, 0};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    r[j >> 2] |= ((uint32_t)code_of(f[j], s) & 0xFFu) << (8 * (j & 3));
+  for (int j = 0; j < 8; ++j) r[j >> 2] |= ((uint32_t)c[j] & 0xFFu) << (8 * (j & 3));
   return r;
 }
 
@@ -78,16 +79,17 @@ w8a8_quantize_kernel(const void* __restrict__ x, int64_t stride, int K, int8_t* 
   mag = max(max(part[0], part[1]), max(part[2], part[3]));
   float s = scale_of(mag);
   if (s == 0.0f) s = 1.0f;
+  const Codes8 q(s);
   int8_t* out = codes + row * (int64_t)K;
 #pragma unroll
   for (int i = 0; i < kHold; ++i) {
     const int k = (i * 256 + tid) * 8;
-    if (k < K) *(u32x2_t*)(out + k) = codes8(f[i], s);
+    if (k < K) *(u32x2_t*)(out + k) = codes8(f[i], q);
   }
   for (int k = (kHold * 256 + tid) * 8; k < K; k += 2048) {
     float g[8];
     load8<DT>(x, base + k, g);
-    *(u32x2_t*)(out + k) = codes8(g, s);
+    *(u32x2_t*)(out + k) = codes8(g, q);
   }
   if (tid == 0) scales[row] = s;
 }
@@ -146,23 +148,25 @@ template <int MT_, int NT_, int WM_, int WN_, int NS_>
 struct Tile {
   static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr int WAVES = WM * WN, BM = 32 * MT * WM, BN = 32 * NT * WN;
-  static constexpr int STAGE = (BM + BN) * 64;           // bytes of one K step of 64
-  static constexpr int LOADS = (BM + BN) / 16 / WAVES;   // 1 KB loads per wave and step
-  static_assert((BM + BN) / 16 % WAVES == 0 && NS >= 4, "whole loads per wave");
+  static constexpr int STAGE = (BM + BN) * 128;         // bytes of one step of 128 codes
+  static constexpr int LOADS = (BM + BN) / 8 / WAVES;   // 1 KB loads per wave and step
+  static_assert((BM + BN) / 8 % WAVES == 0 && NS >= 3, "whole loads per wave");
 };
 
 // One workgroup per BM x BN tile of y on v_mfma_i32_32x32x32_i8, the rows of
 // w as the first operand (so that a lane's 4 consecutive results are 4
-// channels of one token).
+// channels of one token).  For calls of few tiles, which wait for memory:
+// nearly all of LDS is steps under way.
 //
-//  * K goes by in steps of 64 codes.  A step's rows of w and x come straight
-//    into LDS (64-byte rows; the 16-byte chunk q of row r at position
-//    q ^ (r >> 2 & 3), so that 16 lanes reading one chunk of 16 rows meet all
-//    banks), NS steps deep: the loads of step t + NS - 1 go out during step t.
-//  * A step is two halves of 32 codes.  The operands of a half are read while
-//    the products of the half before run, across the step's boundary too: the
-//    wait and the barrier for step t + 1 stand in the middle of step t.
-//  * The results pass through LDS into whole 64 NT-byte rows of y.
+//  * K goes by in steps of 128 codes.  A step's rows of w and x come straight
+//    into LDS (128-byte rows, whole cache lines; the 16-byte chunk q of row r at
+//    position q ^ (r >> 1 & 7), so that 16 lanes reading one chunk of 16 rows
+//    meet all banks), NS steps deep: the loads of step t + NS - 1 go out in
+//    step t.
+//  * A step is four quarters of 32 codes.  The operands of a quarter are read
+//    while the products of the quarter before run, across the step's boundary
+//    too: the wait and the barrier for step t + 1 stand before step t's last.
+//  * The results pass through LDS into whole 64 NT-byte pieces of y's rows.
 template <int DT, class TL>
 __global__ void __launch_bounds__(64 * TL::WAVES)
 w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
@@ -182,35 +186,33 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / TL::WN, wn = wave % TL::WN;
-  const int KT = (K + 63) >> 6;
+  const int KT = (K + 127) >> 7;
   const rsrc_t rw = make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(TL::BN, N - col0) * (uint32_t)K);
   const rsrc_t rx = make_rsrc(xq + (size_t)row0 * K, (uint32_t)min(TL::BM, M - row0) * (uint32_t)K);
 
-  // load i of this wave fills the LDS block WAVES i + wave (16 rows); blocks
-  // below BN / 16 are rows of w
-  const int lrow = lane >> 2, lchunk = (lane & 3) ^ ((lane >> 4) & 3);
-  const uint32_t lane_off = (uint32_t)lrow * (uint32_t)K + 16u * lchunk;
-  // chunks of the last step that lie past K
-  const uint32_t tail = 64 * (KT - 1) + 16 * lchunk >= K ? kOutOfRange : 0u;
+  // load i of this wave fills the LDS block WAVES i + wave (8 rows); blocks
+  // below BN / 8 are rows of w
+  const int lrow = lane >> 3;
   auto load = [&](int t, int i) {
     const int blk = TL::WAVES * i + wave;
-    const bool is_w = blk < TL::BN / 16;
-    const uint32_t row = 16u * (uint32_t)(is_w ? blk : blk - TL::BN / 16);
-    uint32_t off = lane_off + row * (uint32_t)K;
-    off |= t < KT - 1 ? 0u : t == KT - 1 ? tail : kOutOfRange;
-    dma16(is_w ? rw : rx, lds + (t % NS) * TL::STAGE + blk * 1024, off, t * 64);
+    const bool is_w = blk < TL::BN / 8;
+    const uint32_t row = 8u * (uint32_t)(is_w ? blk : blk - TL::BN / 8) + (uint32_t)lrow;
+    const uint32_t chunk = ((uint32_t)lane & 7u) ^ ((row >> 1) & 7u);
+    const uint32_t off =
+        128 * t + 16 * (int)chunk < K ? row * (uint32_t)K + 16u * chunk : kOutOfRange;
+    dma16(is_w ? rw : rx, lds + (t % NS) * TL::STAGE + blk * 1024, off, t * 128);
   };
 
   const int r = lane & 31, h = lane >> 5;
-  const uint32_t swz = (r >> 2) & 3;
-  const uint32_t woff = (uint32_t)(wn * NT * 32 + r) * 64, xoff = (uint32_t)(TL::BN + wm * MT * 32 + r) * 64;
+  const uint32_t swz = (r >> 1) & 7;
+  const uint32_t woff = (uint32_t)(wn * NT * 32 + r) * 128, xoff = (uint32_t)(TL::BN + wm * MT * 32 + r) * 128;
   i32x4_t fw[2][NT], fx[2][MT];
-  auto read = [&](int t, int half, i32x4_t (&w)[NT], i32x4_t (&x)[MT]) {
-    const uint8_t* st = lds + (t % NS) * TL::STAGE + (((2 * half + h) ^ swz) << 4);
+  auto read = [&](int t, int quarter, i32x4_t (&w)[NT], i32x4_t (&x)[MT]) {
+    const uint8_t* st = lds + (t % NS) * TL::STAGE + (((2 * quarter + h) ^ swz) << 4);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) w[i] = *(const i32x4_t*)(st + woff + i * 2048);
+    for (int i = 0; i < NT; ++i) w[i] = *(const i32x4_t*)(st + woff + i * 4096);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) x[i] = *(const i32x4_t*)(st + xoff + i * 2048);
+    for (int i = 0; i < MT; ++i) x[i] = *(const i32x4_t*)(st + xoff + i * 4096);
   };
   i32x16_t acc[NT][MT];
 #pragma unroll
@@ -233,29 +235,24 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 2) * L) : "memory");
   read(0, 0, fw[0], fx[0]);
   for (int t = 0; t < KT; ++t) {
-    read(t, 1, fw[1], fx[1]);
-    products(fw[0], fx[0]);
+    // the slot of step t - 1 is free: every wave has passed the barrier below
+    // with its reads of that step complete
 #pragma unroll
-    for (int k = 0; k < MT * NT; ++k) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one product
-      if (k < (MT + NT + 1) / 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // two reads
+    for (int q = 0; q < 3; ++q) {
+      read(t, q + 1, fw[(q + 1) & 1], fx[(q + 1) & 1]);
+      if (q == 0) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) load(t + NS - 1, i);
+      }
+      products(fw[q & 1], fx[q & 1]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    // step t + 1 is complete in LDS, and every wave is done with step t - 1
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 3) * L) : "memory");
+    // step t + 1 is complete in LDS (the loads of NS - 2 later steps may be
+    // pending), and so are this wave's reads of step t
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * L) : "memory");
     __builtin_amdgcn_sched_barrier(0);
     read(t + 1, 0, fw[0], fx[0]);
-#pragma unroll
-    for (int i = 0; i < L; ++i) load(t + NS - 1, i);
     products(fw[1], fx[1]);
-    // the reads first: a load into LDS may not pass a read before it
-    constexpr int RD = (MT + NT + 1) / 2, PER = (L + MT * NT - RD - 1) / (MT * NT - RD);
-#pragma unroll
-    for (int k = 0; k < MT * NT; ++k) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (k < RD) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      else __builtin_amdgcn_sched_group_barrier(0x020, PER, 0);  // loads
-    }
     __builtin_amdgcn_sched_barrier(0);
   }
   // the loads past the last step have written their zeros
@@ -512,76 +509,227 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   }
 }
 
-// One wave per 32 x 32 tile of y on v_mfma_i32_32x32x32_i8, operands straight
-// from memory: lane l holds 16 codes of row l & 31 at inputs 16 (l >> 5) of a
-// step; rows past the end and inputs past K read 0.
-template <int DT>
-__global__ void __launch_bounds__(256)
-w8a8_gemm_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
-                 const int8_t* __restrict__ wq, const float* __restrict__ sw,
-                 const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
-                 int K) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row0 = (int)blockIdx.y * 64 + 32 * (wave >> 1);
-  const int col0 = (int)blockIdx.x * 64 + 32 * (wave & 1);
-  if (row0 >= M || col0 >= N) return;
-  const int r = lane & 31, h = lane >> 5;
-  const rsrc_t rx = make_rsrc(xq + (size_t)row0 * K, (uint32_t)min(32, M - row0) * (uint32_t)K);
-  const rsrc_t rw = make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(32, N - col0) * (uint32_t)K);
-  i32x16_t acc{};
-  for (int k = 16 * h; k < ((K + 31) & ~31); k += 32) {
-    const uint32_t off = k < K ? (uint32_t)r * (uint32_t)K + (uint32_t)k : kOutOfRange;
-    const i32x4_t a = __builtin_bit_cast(i32x4_t, bld128(rx, off, 0));
-    const i32x4_t b = __builtin_bit_cast(i32x4_t, bld128(rw, off, 0));
-    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc, 0, 0, 0);
-  }
-  const int col = col0 + r;
-  if (col >= N) return;
-  const float t = sw[col], b = bias ? widen16<DT>(bias[col]) : 0.0f;
+// Few tokens: the call is the stream of w.  One workgroup of 8 waves per 16 NT
+// channels and all (at most 16 MB) tokens, on v_mfma_i32_16x16x64_i8; the waves
+// take the steps of 64 codes in turn, straight from memory into registers
+// (lane l: 16 codes of row l & 15), kAhead steps of a wave under way, and their
+// sums are joined in LDS.
+//
+// FUSED: the tokens come in 16 bits, every workgroup quantizes them for itself
+// into LDS while its first rows of w are on their way; each of 512 lanes holds
+// 8 values of up to kRows rows of 4096 (a longer row counts as several).
+constexpr int kAhead = 4, kRows = 4;
+
+template <int DT, int MB, int NT, bool FUSED>
+__global__ void __launch_bounds__(512)
+w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __restrict__ sx,
+                   const int8_t* __restrict__ wq, const float* __restrict__ sw,
+                   const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
+                   int K) {
+  constexpr int kSum = 8 * NT * MB * 1024, kCodes = FUSED ? kRows * 4096 + 16 * 16 : 0;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kSum > kCodes ? kSum : kCodes];
+  __shared__ uint32_t mags[FUSED ? kRows : 1][8];
+  __shared__ float scales[16 * MB];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int col0 = (int)blockIdx.x * 16 * NT;
+  const int KT = (K + 63) >> 6;
+  const rsrc_t rw = make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(16 * NT, N - col0) * (uint32_t)K);
+  const uint32_t lane_off = (uint32_t)r * (uint32_t)K + 16u * g;
+  auto load_w = [&](int s, i32x4_t (&w)[NT]) {
+    const bool in = 64 * s + 16 * g < K;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = row0 + (i & 3) + 4 * h + 8 * (i >> 2);
-    if (row < M) out[(size_t)row * N + col] = round16<DT>(result(acc[i], sx[row], t, b));
+    for (int i = 0; i < NT; ++i)
+      w[i] = __builtin_bit_cast(
+          i32x4_t, bld128(rw, in ? lane_off + (uint32_t)(16 * i) * (uint32_t)K : kOutOfRange, s * 64));
+  };
+  i32x4_t w[kAhead][NT];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load_w(wave + 8 * u, w[u]);
+
+  rsrc_t rx;
+  const int pitch = K + 16;  // FUSED: bytes of a row of codes in LDS
+  if constexpr (FUSED) {
+    const int per = (K + 4095) >> 12;  // pieces of 4096 per row
+    u32x4_t raw[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int m = i / per, k = (i % per) * 4096 + tid * 8;
+      raw[i] = u32x4_t{0, 0, 0, 0};
+      if (m < M && k < K) raw[i] = *(const u32x4_t*)((const uint16_t*)x + m * x_stride + k);
+      uint32_t mag = 0;
+      float f[8];
+      widen8<DT>(raw[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mag = max(mag, mag_bits(f[j]));
+      mag = lanes_max<64>(mag);
+      if (lane == 0) mags[i][wave] = mag;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int m = i / per, k = (i % per) * 4096 + tid * 8;
+      if (m >= M) break;
+      uint32_t mag = 0;
+      for (int p = m * per; p < (m + 1) * per; ++p)
+#pragma unroll
+        for (int v = 0; v < 8; ++v) mag = max(mag, mags[p][v]);
+      float s = scale_of(mag);
+      if (s == 0.0f) s = 1.0f;
+      if (k < K) {
+        float f[8];
+        widen8<DT>(raw[i], f);
+        *(u32x2_t*)(lds + m * pitch + k) = codes8(f, Codes8(s));
+      }
+      if (tid == 0) scales[m] = s;
+    }
+    __syncthreads();
+  } else {
+    rx = make_rsrc(x, (uint32_t)M * (uint32_t)K);
+    if (tid < 16 * MB) scales[tid] = tid < M ? sx[tid] : 0.0f;
+  }
+  // tokens past the last repeat it (their results are not written)
+  auto load_x = [&](int s, i32x4_t (&v)[MB]) {
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int m = min(16 * j + r, M - 1);
+      if constexpr (FUSED)
+        v[j] = *(const i32x4_t*)(lds + m * pitch + min(64 * s + 16 * g, K - 16));
+      else
+        v[j] = __builtin_bit_cast(
+            i32x4_t, bld128(rx, 64 * s + 16 * g < K ? (uint32_t)m * (uint32_t)K + 16u * g : kOutOfRange,
+                            s * 64));
+    }
+  };
+  i32x4_t xv[kAhead][MB];
+  if constexpr (!FUSED) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load_x(wave + 8 * u, xv[u]);
+  }
+
+  i32x4_t acc[NT][MB];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MB; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  for (int s0 = wave; s0 < KT; s0 += 8 * kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if constexpr (FUSED) load_x(s0 + 8 * u, xv[u]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][i], xv[u][j], acc[i][j], 0, 0, 0);
+      load_w(s0 + 8 * (u + kAhead), w[u]);
+      if constexpr (!FUSED) load_x(s0 + 8 * (u + kAhead), xv[u]);
+    }
+  }
+
+  // ---- join: lane holds channels 4 g .. 4 g + 3 of token r of each product
+  if constexpr (FUSED) __syncthreads();  // the codes have been read
+  i32x4_t* part = (i32x4_t*)lds;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MB; ++j) part[((wave * NT + i) * MB + j) * 64 + r * 4 + g] = acc[i][j];
+  __syncthreads();
+  for (int e = tid; e < NT * MB * 64; e += 512) {
+    const int i = e / (64 * MB), j = e / 64 % MB, m = 16 * j + (e % 64) / 4, n = col0 + 16 * i + 4 * (e % 4);
+    i32x4_t v = part[e];
+#pragma unroll
+    for (int p = 1; p < 8; ++p) v += part[p * NT * MB * 64 + e];
+    if (m < M && n < N) {
+      const float4_t t = *(const float4_t*)(sw + n);
+      float y[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+        y[a] = result(v[a], scales[m], t[a], bias ? widen16<DT>(bias[n + a]) : 0.0f);
+      *(u32x2_t*)(out + (size_t)m * N + n) = u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
+    }
   }
 }
 
-typedef Tile<4, 4, 2, 2, 5> T256;
+// --------------------------------------------------------------- dispatch ---
 typedef Tile<2, 2, 2, 2, 4> T128;
 
+// The operands of a call: 16-bit rows (with a stride) or codes with scales.
+struct Args {
+  const void* x;
+  int64_t x_stride;
+  const float* sx;
+  const int8_t* wq;
+  const float* sw;
+  const uint16_t* bias;
+  uint16_t* out;
+  int M, N, K;
+};
+
 template <int DT, class TL>
-void launch_tile(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
-                 const void* bias, void* out, int64_t M, int64_t N, int64_t K, hipStream_t st) {
-  const int mb = (int)ceil_div(M, TL::BM), nb = (int)ceil_div(N, TL::BN);
+void launch_tile(const Args& a, hipStream_t st) {
+  const int mb = (int)ceil_div(a.M, TL::BM), nb = (int)ceil_div(a.N, TL::BN);
   const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
   launch_timed(w8a8_tile_kernel<DT, TL>, dim3((unsigned)per_xcd * 8), dim3(64 * TL::WAVES), 0, st,
-               xq, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K, mb,
-               nb, per_xcd);
+               (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb, per_xcd);
 }
 
+template <int DT, int MB, int NT, bool FUSED>
+void launch_stream(const Args& a, hipStream_t st) {
+  launch_timed(w8a8_stream_kernel<DT, MB, NT, FUSED>, dim3((unsigned)ceil_div(a.N, 16 * NT)),
+               dim3(512), 0, st, a.x, a.x_stride, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K);
+}
+
+// Channels per workgroup of the stream kernel: 64 where that leaves two
+// workgroups for each of 256 CUs, else 32, else 16.
+int stream_nt(int64_t N) { return N >= 512 * 64 ? 4 : N >= 512 * 32 ? 2 : 1; }
+
+template <int DT, int MB, bool FUSED>
+void launch_stream_nt(const Args& a, hipStream_t st) {
+  const int nt = stream_nt(a.N);
+  if (nt == 4 && MB <= 2) launch_stream<DT, MB, MB <= 2 ? 4 : 2, FUSED>(a, st);
+  else if (nt >= 2) launch_stream<DT, MB, 2, FUSED>(a, st);
+  else launch_stream<DT, MB, 1, FUSED>(a, st);
+}
+
+// Whether w8a8_linear quantizes inside the product.
+bool fused(int64_t M, int64_t K) { return M * ceil_div(K, 4096) <= kRows; }
+
 template <int DT>
-hipError_t launch_gemm_dt(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
-                          const void* bias, void* out, int64_t M, int64_t N, int64_t K,
-                          hipStream_t st) {
-  if (M > 256) {
-    const int mb = (int)ceil_div(M, 256), nb = (int)ceil_div(N, 256);
+hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
+  if (a.M > 512) {
+    const int mb = (int)ceil_div(a.M, 256), nb = (int)ceil_div(a.N, 256);
     const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
     launch_timed(w8a8_wide_kernel<DT>, dim3((unsigned)std::min(256, per_xcd * 8)), dim3(256), 0, st,
-                 xq, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K, mb,
-                 nb, per_xcd);
+                 (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb,
+                 per_xcd);
+  } else if (a.M > 64) {
+    launch_tile<DT, T128>(a, st);
+  } else if (a.M > 32) {
+    launch_stream_nt<DT, 4, false>(a, st);
+  } else if (a.M > 16) {
+    launch_stream_nt<DT, 2, false>(a, st);
+  } else {
+    launch_stream_nt<DT, 1, false>(a, st);
   }
-  else if (M > 64) launch_tile<DT, T128>(xq, sx, wq, sw, bias, out, M, N, K, st);
-  else
-    launch_timed(w8a8_gemm_kernel<DT>, dim3((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64)),
-                 dim3(256), 0, st, xq, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M,
-                 (int)N, (int)K);
   return hipGetLastError();
 }
 
 hipError_t launch_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                        const void* bias, void* out, int64_t M, int64_t N, int64_t K, int dtype,
                        hipStream_t st) {
-  return (dtype == DT_F16 ? launch_gemm_dt<DT_F16> : launch_gemm_dt<DT_BF16>)(
-      xq, sx, wq, sw, bias, out, M, N, K, st);
+  const Args a = {xq, K, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K};
+  return (dtype == DT_F16 ? launch_gemm_dt<DT_F16> : launch_gemm_dt<DT_BF16>)(a, st);
+}
+
+hipError_t launch_fused(const void* x, int64_t x_stride, const int8_t* wq, const float* sw,
+                        const void* bias, void* out, int64_t M, int64_t N, int64_t K, int dtype,
+                        hipStream_t st) {
+  const Args a = {x, x_stride, nullptr, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M,
+                  (int)N, (int)K};
+  if (dtype == DT_F16) launch_stream_nt<DT_F16, 1, true>(a, st);
+  else launch_stream_nt<DT_BF16, 1, true>(a, st);
+  return hipGetLastError();
 }
 
 // --------------------------------------------------------------- checking ---
@@ -621,7 +769,7 @@ int w8a8_quantize(const void* x, int64_t M, int64_t K, int64_t x_stride, int32_t
 
 int64_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t linear) {
   if (validate_shape(M, N, K) != W4A16_OK) return -1;
-  return linear ? linear_bytes(M, K) : 0;
+  return linear && !fused(M, K) ? linear_bytes(M, K) : 0;
 }
 
 int w8a8_gemm(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
@@ -653,6 +801,8 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
     if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
     clear_pending_error();
     const hipStream_t st = (hipStream_t)stream;
+    if (fused(M, K))
+      return hip_status(launch_fused(x, x_stride, wq, w_scale, bias, out, M, N, K, dtype, st));
     int8_t* xq = (int8_t*)workspace;
     float* sx = (float*)(xq + pad256(M * K));
     if (int s = hip_status(launch_quantize(x, M, K, x_stride, dtype, xq, sx, st))) return s;
