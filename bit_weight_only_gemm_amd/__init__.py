@@ -35,8 +35,11 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The raw handle of a stream (the current one's without a Stream object
+    in between, whose making costs more than a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t, dtype, name, numel=None):
@@ -366,12 +369,13 @@ _WS = {}
 
 
 def _ws_cache(device, nbytes, stream=None):
-    st = torch.cuda.current_stream() if stream is None else stream
-    key = (str(device), st.cuda_stream)
+    key = (device, _stream(stream))
     cur = _WS.get(key)
     if cur is None or cur.numel() * 4 < nbytes:
+        st = torch.cuda.current_stream() if stream is None else stream
         st.synchronize()
-        cur = workspace(max(nbytes, 1 << 20), device)
+        with torch.cuda.stream(st):     # a block of the stream that uses it
+            cur = workspace(max(nbytes, 1 << 20), device)
         _WS[key] = cur
     return cur
 

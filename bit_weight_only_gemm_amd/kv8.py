@@ -16,8 +16,8 @@ import math
 
 import torch
 
-from . import _DT, _lib, _need, _ptr, _stream
-from .w8a8 import _empty, _space
+from . import _DT, _lib, _need, _stream
+from .w8a8 import _at, _empty, _space
 
 
 def kv8_cache(num_pages, page_size, kv_heads, head_dim, device="cuda"):
@@ -51,12 +51,14 @@ def _heads(t, dtype, name, tokens=None, heads=None, D=None):
         raise TypeError("%s must be %s, got %s" % (name, dtype or "float16 or bfloat16", t.dtype))
     if t.dim() != 3:
         raise ValueError("%s must be [tokens, heads, D]" % name)
-    want = (t.shape[0] if tokens is None else tokens, t.shape[1] if heads is None else heads, D)
-    if tuple(t.shape) != want:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), want))
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+    n, h, d = t.shape
+    if d != D or (tokens is not None and n != tokens) or (heads is not None and h != heads):
+        raise ValueError("%s has shape %s, expected [%s, %s, %d]"
+                         % (name, tuple(t.shape), tokens or "tokens", heads or "heads", D))
+    step, head, one = t.stride()
+    if n and (one != 1 or (h > 1 and head != D)):
         raise ValueError("%s must be contiguous within a token" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    return step if n > 1 else h * D
 
 
 def _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens):
@@ -103,9 +105,9 @@ def kv8_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, max_new=None,
             raise ValueError("cos must be [positions, rope_dim / 2]")
         rows, dim = cos.shape[0], 2 * cos.shape[1]
     _lib.check(_lib.lib().kv8_append(
-        _ptr(q), q_stride, _ptr(q_out), o_stride, _ptr(k), k_stride, _ptr(v), v_stride,
-        _ptr(cache["k"]), _ptr(cache["v"]), _ptr(cache["k_scale"]), _ptr(cache["v_scale"]), pages,
-        T, _ptr(page_table), width, _ptr(seq_lens), _ptr(cu_seqlens), _ptr(cos), _ptr(sin), rows,
+        _at(q), q_stride, _at(q_out), o_stride, _at(k), k_stride, _at(v), v_stride,
+        _at(cache["k"]), _at(cache["v"]), _at(cache["k_scale"]), _at(cache["v_scale"]), pages,
+        T, _at(page_table), width, _at(seq_lens), _at(cu_seqlens), _at(cos), _at(sin), rows,
         dim, int(interleaved), tokens, B, max_new, H, Hkv, D, _DT[k.dtype], _stream(stream)),
         "kv8_append")
     return q_out
@@ -121,8 +123,8 @@ def kv8_dequant(cache, pages, dtype=torch.bfloat16, stream=None):
     k = _empty((n, Hkv, T, D), dtype, pages.device, stream)
     v = _empty((n, Hkv, T, D), dtype, pages.device, stream)
     _lib.check(_lib.lib().kv8_dequant(
-        _ptr(cache["k"]), _ptr(cache["v"]), _ptr(cache["k_scale"]), _ptr(cache["v_scale"]), num, T,
-        Hkv, D, _ptr(pages), n, _DT[dtype], _ptr(k), _ptr(v), _stream(stream)), "kv8_dequant")
+        _at(cache["k"]), _at(cache["v"]), _at(cache["k_scale"]), _at(cache["v_scale"]), num, T,
+        Hkv, D, _at(pages), n, _DT[dtype], _at(k), _at(v), _stream(stream)), "kv8_dequant")
     return k, v
 
 
@@ -154,9 +156,9 @@ def kv8_attention(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
     need = max(0, int(L.kv8_attention_workspace_bytes(tokens, B, max_new, max_len, H, Hkv, D)))
     workspace, nbytes = _space(workspace, need, q.device, stream)
     _lib.check(L.kv8_attention(
-        _ptr(q), q_stride, _ptr(cache["k"]), _ptr(cache["v"]), _ptr(cache["k_scale"]),
-        _ptr(cache["v_scale"]), pages, T, _ptr(page_table), width, _ptr(seq_lens),
-        _ptr(cu_seqlens), 1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
-        _ptr(out), o_stride, _ptr(lse), tokens, B, max_new, max_len, H, Hkv, D, _DT[q.dtype],
-        _ptr(workspace), nbytes, _stream(stream)), "kv8_attention")
+        _at(q), q_stride, _at(cache["k"]), _at(cache["v"]), _at(cache["k_scale"]),
+        _at(cache["v_scale"]), pages, T, _at(page_table), width, _at(seq_lens),
+        _at(cu_seqlens), 1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
+        _at(out), o_stride, _at(lse), tokens, B, max_new, max_len, H, Hkv, D, _DT[q.dtype],
+        _at(workspace), nbytes, _stream(stream)), "kv8_attention")
     return out

@@ -10,11 +10,9 @@ or, for rows quantized once and used by several layers:
     y = w8a8_gemm(xq, xs, wq, ws, dtype=torch.bfloat16)
 """
 
-import contextlib
-
 import torch
 
-from . import _DT, _lib, _need, _ptr, _stream, _ws_cache
+from . import _DT, _lib, _need, _stream, _ws_cache
 
 _QDT = dict(_DT)
 _QDT[torch.float32] = 2
@@ -23,8 +21,9 @@ _QDT[torch.float32] = 2
 def _empty(shape, dtype, device, stream=None):
     """An output tensor of the stream that the kernel runs on (the caching
     allocator reuses a block in the order of its own stream)."""
-    on = contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-    with on:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -35,23 +34,25 @@ def _rows(t, dtypes, name, K=None):
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(map(str, dtypes)), t.dtype))
-    if t.dim() < 1 or t.shape[-1] == 0:
+    shape = t.shape
+    if len(shape) < 1 or shape[-1] == 0:
         raise ValueError("%s has no columns" % name)
-    if K is not None and t.shape[-1] != K:
-        raise ValueError("%s last dim %d != K %d" % (name, t.shape[-1], K))
-    if t.dim() != 2 or t.stride(1) != 1:
-        t = _flat(t, name)
-    return t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    if K is not None and shape[-1] != K:
+        raise ValueError("%s last dim %d != K %d" % (name, shape[-1], K))
+    if len(shape) != 2:
+        try:
+            t = t.view(-1, shape[-1])
+        except RuntimeError:
+            raise ValueError("%s must have evenly spaced rows" % name) from None
+    step, one = t.stride()
+    if one != 1 and shape[-1] > 1:
+        raise ValueError("%s must be contiguous within a row" % name)
+    M = t.shape[0]
+    return M, shape[-1], max(step, shape[-1]) if M > 1 else shape[-1]
 
 
-def _flat(t, name):
-    try:
-        t = t.view(-1, t.shape[-1])
-    except RuntimeError:
-        t = None
-    if t is None or t.stride(1) != 1:
-        raise ValueError("%s must have evenly spaced rows, contiguous within a row" % name)
-    return t
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def w8a8_workspace_bytes(M, N, K, linear=True):
@@ -68,8 +69,8 @@ def w8a8_quantize(x, stream=None):
     M, K, stride = _rows(x, tuple(_QDT), "x")
     codes = _empty(x.shape, torch.int8, x.device, stream)
     scales = _empty(x.shape[:-1], torch.float32, x.device, stream)
-    _lib.check(_lib.lib().w8a8_quantize(_ptr(x), M, K, stride, _QDT[x.dtype], _ptr(codes),
-                                        _ptr(scales), _stream(stream)), "w8a8_quantize")
+    _lib.check(_lib.lib().w8a8_quantize(_at(x), M, K, stride, _QDT[x.dtype], _at(codes),
+                                        _at(scales), _stream(stream)), "w8a8_quantize")
     return codes, scales
 
 
@@ -120,8 +121,8 @@ def w8a8_gemm(xq, x_scale, wq, w_scale, bias=None, dtype=torch.bfloat16, out=Non
         workspace, nbytes = _space(workspace, need, xq.device, stream)
     else:
         workspace = None
-    _lib.check(_lib.lib().w8a8_gemm(_ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias),
-                                    _ptr(out), M, N, K, _DT[dtype], _ptr(workspace), nbytes,
+    _lib.check(_lib.lib().w8a8_gemm(_at(xq), _at(x_scale), _at(wq), _at(w_scale), _at(bias),
+                                    _at(out), M, N, K, _DT[dtype], _at(workspace), nbytes,
                                     _stream(stream)), "w8a8_gemm")
     return out
 
@@ -134,7 +135,7 @@ def w8a8_linear(x, wq, w_scale, bias=None, out=None, workspace=None, stream=None
     out = _output(out, (*x.shape[:-1], N), x.dtype, x.device, stream)
     need = max(0, int(_lib.lib().w8a8_workspace_bytes(M, N, K, 1)))
     workspace, nbytes = _space(workspace, need, x.device, stream)
-    _lib.check(_lib.lib().w8a8_linear(_ptr(x), stride, _ptr(wq), _ptr(w_scale), _ptr(bias),
-                                      _ptr(out), M, N, K, _DT[x.dtype], _ptr(workspace), nbytes,
+    _lib.check(_lib.lib().w8a8_linear(_at(x), stride, _at(wq), _at(w_scale), _at(bias),
+                                      _at(out), M, N, K, _DT[x.dtype], _at(workspace), nbytes,
                                       _stream(stream)), "w8a8_linear")
     return out
