@@ -10,6 +10,8 @@
 // applied in fp32: the keys' to the scores, the values' to the sum over 64
 // tokens.  Probabilities are rounded to fp16 (to nearest) for the second
 // product, their sum is taken before that rounding.
+#include <type_traits>
+
 #include "kv8.h"
 #include "launch.h"
 
@@ -18,6 +20,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kUnit = 64;  // tokens a wave takes at a time
+
+typedef float float16_t __attribute__((ext_vector_type(16)));
 
 // 8 codes of two dwords as an fp16 operand: 0x6400 | c is 1024 + c.
 __device__ __forceinline__ half8_t codes_f16(uint32_t a, uint32_t b) {
@@ -32,13 +36,45 @@ __device__ __forceinline__ half8_t codes_f16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(half8_t, r);
 }
 
+// A row of queries as fp16 operands: N pieces of 8 channels in each of the
+// lanes l, l ^ FIRST, .. that hold the row (FIRST = 16: four lanes, 32: two).
+// fp16 rows as they are; bf16 rows times a power of two that brings the row's
+// largest magnitude to [2^14, 2^15), held to fp32's normal range.  What the
+// scores have to be multiplied by.
+template <int DT, int N, int FIRST>
+__device__ __forceinline__ float queries_f16(const u32x4_t (&w)[N], half8_t (&out)[N]) {
+  if constexpr (DT == DT_F16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = __builtin_bit_cast(half8_t, w[i]);
+    return 1.0f;
+  } else {
+    uint32_t mag = 0;
+    float f[N][8];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      widen8<DT>(w[i], f[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mag = max(mag, mag_bits(f[i][j]));
+    }
+#pragma unroll
+    for (int o = FIRST; o < 64; o <<= 1) mag = max(mag, (uint32_t)__shfl_xor((int)mag, o, 64));
+    const int e2 = clamp_int((int)(mag >> 23) - 127, -100, 126);
+    const float up = __builtin_bit_cast(float, (uint32_t)(127 + 14 - e2) << 23);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[i][j] = (_Float16)(f[i][j] * up);
+    return __builtin_bit_cast(float, (uint32_t)(127 - 14 + e2) << 23);
+  }
+}
+
 // Query rows of a (sequence, kv head): row i is token i / G, head i % G.  A
-// row tile is 16 of them; it sees keys up to the largest limit of its rows.
+// row tile is `rows` of them; it sees keys up to the largest limit of its rows.
 __device__ __forceinline__ int row_limit(const Kv8Seq& s, int causal, int j) {
   return causal ? clamp_int(s.len - s.n + j + 1, 0, s.len) : s.len;
 }
-__device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, int G) {
-  return row_limit(s, causal, min((rt * 16 + 15) / G, s.n - 1));
+__device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, int rows, int G) {
+  return row_limit(s, causal, min((rt * rows + rows - 1) / G, s.n - 1));
 }
 
 // Partial results of a split: O [row][split][D], then (m, l) [row][split],
@@ -73,7 +109,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const int G = c.H / c.Hkv;
   const Kv8Seq seq = kv8_seq(c, b);
   if (rt * 16 >= seq.n * G) return;
-  const int top = tile_limit(seq, causal, rt, G);
+  const int top = tile_limit(seq, causal, rt, 16, G);
   const int nu = (top + kUnit - 1) / kUnit;
   const int u0 = split * units, u1 = min(u0 + units, nu);
   if (split > 0 && u0 >= nu) return;
@@ -88,44 +124,16 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   float rowscale = scale * kLog2e;
   {
     const uint16_t* qp = q + (int64_t)tok * q_stride + head * D + 16 * g;
-    u32x4_t w[DC][2];
+    u32x4_t w[2 * DC];
 #pragma unroll
-    for (int i = 0; i < DC; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        w[i][e] = u32x4_t{0, 0, 0, 0};
-        if (rv) w[i][e] = *(const u32x4_t*)(qp + 64 * i + 8 * e);
-      }
-    if constexpr (DT == DT_F16) {
-#pragma unroll
-      for (int i = 0; i < DC; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) qf[i][e] = __builtin_bit_cast(half8_t, w[i][e]);
-    } else {
-      uint32_t mag = 0;
-      float f[DC][2][8];
-#pragma unroll
-      for (int i = 0; i < DC; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          widen8<DT>(w[i][e], f[i][e]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) mag = max(mag, mag_bits(f[i][e][j]));
-        }
-      mag = max(mag, (uint32_t)__shfl_xor((int)mag, 16, 64));
-      mag = max(mag, (uint32_t)__shfl_xor((int)mag, 32, 64));
-      // exponent of the row's largest magnitude; 2^(14 - e) brings it to
-      // [2^14, 2^15), held to the normal fp32 range
-      const int e2 = clamp_int((int)(mag >> 23) - 127, -100, 126);
-      const float up = __builtin_bit_cast(float, (uint32_t)(127 + 14 - e2) << 23);
-      rowscale *= __builtin_bit_cast(float, (uint32_t)(127 - 14 + e2) << 23);
-#pragma unroll
-      for (int i = 0; i < DC; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) qf[i][e][j] = (_Float16)(f[i][e][j] * up);
+    for (int i = 0; i < 2 * DC; ++i) {
+      w[i] = u32x4_t{0, 0, 0, 0};
+      if (rv) w[i] = *(const u32x4_t*)(qp + 64 * (i >> 1) + 8 * (i & 1));
     }
+    half8_t f[2 * DC];
+    rowscale *= queries_f16<DT, 2 * DC, 16>(w, f);
+#pragma unroll
+    for (int i = 0; i < 2 * DC; ++i) qf[i >> 1][i & 1] = f[i];
   }
 
   float m = -INFINITY, l = 0.0f;
@@ -187,7 +195,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       for (int i = 0; i < 4; ++i) {
         const float p = __builtin_amdgcn_exp2f(s[a][i] - ms);
         sum += p;
-        pf[a >> 1][4 * (a & 1) + i] = (_Float16)(p * rel);
+        pf[a >> 1][4 * (a & 1) + i] = (_Float16)(p == 0.0f ? 0.0f : p * rel);
       }
     l = l * alpha + sum;
 #pragma unroll
@@ -252,11 +260,394 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     lse[tk * c.H + hd] = ll == 0.0f ? -INFINITY : (mm + __log2f(ll)) * kLn2;
 }
 
+// The larger of the values that lanes l and l ^ 32 hold.
+__device__ __forceinline__ float both_halves_max(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__builtin_bit_cast(float, r[0]), __builtin_bit_cast(float, r[1]));
+}
+
+// Position of a key row's 16-byte chunks in LDS (rows of 2 D bytes): 16 lanes
+// that read one chunk of 16 rows meet all banks.
+template <int D>
+__device__ __forceinline__ int swizzle(int row) {
+  return D == 128 ? row & 15 : (row >> 1) & 7;
+}
+
+// The products of many rows: W waves, each 32 rows, share the conversion of
+// the keys and values of a unit of 64 tokens to fp16 in LDS.
+//
+//  * v_mfma_f32_32x32x16_f16.  Scores come out as S^T; the keys' rows are
+//    permuted so that lane l (half h = l >> 5) holds tokens 16 h + i of each 32
+//    in register i, the operand layout of the second product, O^T += V^T P^T.
+//  * The scores of the next unit are formed while this one's become
+//    probabilities, and later units' codes are staged while the second product
+//    runs: a wave's matrix and vector instructions alternate.
+//  * A unit's codes are loaded into registers a unit before they are turned to
+//    fp16 and written to LDS, its scales and page numbers ahead of those.
+//    Keys: rows of 2 D bytes, their 16-byte chunks permuted by row; values:
+//    [16 tokens][8 of them][channel] pieces of 16 bytes.  Reads and writes meet
+//    all banks.
+//  * The running maximum m of a row moves only when a score passes it by 2^8
+//    (fp16 holds the probabilities up to then); so does the reference u that
+//    the values' page scales are taken relative to, by 2^4.  A probability
+//    enters the second product as w = exp2(s - m + log2(vs / u)) and the sum as
+//    w (u / vs); vs / u is held to 2^-30 and up, below which w is 0 in fp16.
+//
+// WHOLE: pages of 64 tokens and more, a unit lies in one page.
+template <int DT, int D, int W, bool WHOLE>
+__global__ void __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(1, 2)))
+kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float scale, int causal,
+                  uint16_t* __restrict__ out, int64_t out_stride, float* __restrict__ lse,
+                  Parts parts, int row_tiles, int splits, int units) {
+  // in iteration u the keys of u + 1 and the values of u are read, and both of
+  // u + 2 written
+  constexpr int NBK = 2, NBV = 3;
+  constexpr int KS = D / 16, DN = D / 32, ROWS = 32 * W;
+  constexpr int BUF = kUnit * D * 2;                // fp16 keys (or values) of a unit
+  constexpr int CH = kUnit * D / 16 / (64 * W);     // 16-byte pieces of each per lane
+  static_assert(CH >= 1, "a piece for every lane");
+  // two waves to a SIMD: 256 registers each, the queries wait in LDS
+  constexpr bool Q_LDS = W == 8;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[(NBK + NBV) * BUF + (Q_LDS ? ROWS * D * 2 : 0)];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, h = lane >> 5;
+  // workgroups go to the 8 XCDs in turn: all row tiles of one (split, sequence,
+  // kv head) go to one of them and share their keys in its cache; the last
+  // tiles, which see the most, first
+  const int groups = c.B * c.Hkv * splits, per_xcd = (groups + 7) >> 3;
+  const int at = (int)(blockIdx.x >> 3);
+  const int grp = at % per_xcd * 8 + (int)(blockIdx.x & 7);
+  if (grp >= groups) return;
+  const int rt = row_tiles - 1 - at / per_xcd;
+  const int hk = grp % c.Hkv, b = grp / c.Hkv % c.B, split = grp / c.Hkv / c.B;
+  const int G = c.H / c.Hkv;
+  const Kv8Seq seq = kv8_seq(c, b);
+  if (rt * ROWS >= seq.n * G) return;
+  const int top = tile_limit(seq, causal, rt, ROWS, G);
+  const int nu = (top + kUnit - 1) / kUnit;
+  const int u0 = split * units, u1 = min(u0 + units, nu);
+  if (split > 0 && u0 >= nu) return;
+
+  const int row0 = rt * ROWS + wave * 32, ridx = row0 + col;
+  const bool rv = ridx < seq.n * G;
+  const int tok = seq.tok + (rv ? ridx / G : 0), head = hk * G + (rv ? ridx % G : 0);
+  const int lim = rv ? row_limit(seq, causal, ridx / G) : 0;
+  // keys that every row of this wave sees, and that any does
+  const int lim_all = row0 + 31 < seq.n * G ? row_limit(seq, causal, row0 / G) : 0;
+  const int lim_any =
+      row0 < seq.n * G ? row_limit(seq, causal, min(row0 + 31, seq.n * G - 1) / G) : 0;
+
+  half8_t qf[Q_LDS ? 1 : KS];
+  uint8_t* q_mine = lds + (NBK + NBV) * BUF + (wave * KS * 64 + lane) * 16;
+  auto query = [&](int i) {
+    if constexpr (Q_LDS) return *(const half8_t*)(q_mine + i * 1024);
+    else return qf[i];
+  };
+  float f_row = scale * kLog2e;
+  {
+    u32x4_t w[KS];
+    half8_t f[KS];
+    const uint16_t* qp = q + (int64_t)tok * q_stride + head * D + 8 * h;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      w[i] = u32x4_t{0, 0, 0, 0};
+      if (rv) w[i] = *(const u32x4_t*)(qp + 16 * i);
+      if (scale < 0.0f) w[i] ^= 0x80008000u;  // the scores' factor is kept positive
+    }
+    f_row = fabsf(f_row) * queries_f16<DT, KS, 32>(w, f);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      if constexpr (Q_LDS) *(half8_t*)(q_mine + i * 1024) = f[i];
+      else qf[i] = f[i];
+    }
+  }
+
+  // ---- staging: piece i of this lane is 16 bytes at 16 (64 W i + tid) of the
+  // unit's [4 subtiles][16 D]
+  const int64_t page_bytes = (int64_t)D << c.lgT;
+  const int T = 1 << c.lgT;
+  const int32_t* table = c.table + (int64_t)b * c.width;
+  u32x4_t kw[CH], vw[CH];
+  // table entries of this lane's pieces of a unit, and of its 16 tokens of
+  // each 32 (WHOLE: one for all), units past the last repeating it; they are
+  // brought into range where they are used, a unit later
+  constexpr int NP = WHOLE ? 1 : CH, NSC = WHOLE ? 1 : 2;
+  int of_piece[NP], of_scale[NSC];
+  auto entry = [&](int u, int token) {
+    return table[min((min(u, nu - 1) * kUnit + token) >> c.lgT, c.width - 1)];
+  };
+  auto turn_pages = [&](int u_pieces, int u_scales) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      of_piece[i] = entry(u_pieces, WHOLE ? 0 : 16 * ((64 * W * i + tid) / D));
+#pragma unroll
+    for (int a = 0; a < NSC; ++a) of_scale[a] = entry(u_scales, WHOLE ? 0 : 32 * a + 16 * h);
+  };
+  // (the empty statements hold a loaded value's first use where it stands)
+  auto fetch = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) asm volatile("" : "+v"(of_piece[i]));
+    if constexpr (WHOLE) {
+      const int page = clamp_int(__builtin_amdgcn_readfirstlane(of_piece[0]), 0, c.pages - 1);
+      const int64_t from = ((int64_t)page * c.Hkv + hk) * page_bytes +
+                           (int64_t)((min(u, nu - 1) * kUnit) & (T - 1)) * D;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        kw[i] = *(const u32x4_t*)(c.k + from + (64 * W * i + tid) * 16);
+        vw[i] = *(const u32x4_t*)(c.v + from + (64 * W * i + tid) * 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int byte = (64 * W * i + tid) * 16, sub = byte / (16 * D);
+        const int t = min(u, nu - 1) * kUnit + 16 * sub;
+        const int64_t from = ((int64_t)clamp_int(of_piece[i], 0, c.pages - 1) * c.Hkv + hk) * page_bytes +
+                             (t & (T - 1)) * D + byte % (16 * D);
+        kw[i] = *(const u32x4_t*)(c.k + from);
+        vw[i] = *(const u32x4_t*)(c.v + from);
+      }
+    }
+  };
+  float ks_next[NSC], vs_next[NSC];
+  auto fetch_scales = [&]() {
+#pragma unroll
+    for (int a = 0; a < NSC; ++a) {
+      asm volatile("" : "+v"(of_scale[a]));
+      const int64_t at_s = (int64_t)clamp_int(of_scale[a], 0, c.pages - 1) * c.Hkv + hk;
+      ks_next[a] = c.ks[at_s];
+      vs_next[a] = c.vs[at_s];
+    }
+  };
+  // part j of CH * 4: half a piece of keys or values to its buffer.  A key
+  // (token 16 sub + tk of the unit) is row 32 (sub >> 1) + the bits of its place
+  // in 32 tokens in the order 0, 1, subtile's parity, 2, 3.  Where the pieces
+  // lie whole 32s of tokens apart, one address of each kind serves them all.
+  auto key_place = [&](int i) {
+    const int byte = (64 * W * i + tid) * 16, sub = byte / (16 * D);
+    const int tk = byte % (16 * D) / D, ch = byte % D / 16;
+    const int row = 32 * (sub >> 1) + (tk & 3) + 4 * (sub & 1) + 8 * (tk >> 2);
+    return row * D * 2 + (((2 * ch) ^ swizzle<D>(row)) << 4);
+  };
+  constexpr bool EVEN = 64 * W * 16 % (32 * D) == 0;
+  int k_place = key_place(0), v_place = (tid / D * 2 * D + tid % D) * 16;
+  auto stage = [&](int j, int kbuf, int vbuf) {
+    const int i = j >> 2, e = j & 1;
+    if (j & 2) {  // a channel's tokens 16 sub + 8 e ..
+      *(half8_t*)(lds + (NBK + vbuf) * BUF + v_place + (64 * W / D * i * 2 + e) * D * 16) =
+          codes_f16(vw[i][2 * e], vw[i][2 * e + 1]);
+    } else {      // a token's channels 16 ch + 8 e ..
+      const int at_k = EVEN ? k_place + 64 * W * 32 * i : key_place(i);
+      *(half8_t*)(lds + kbuf * BUF + (at_k ^ e << 4)) = codes_f16(kw[i][2 * e], kw[i][2 * e + 1]);
+    }
+  };
+
+  float m = -1e30f, l = 0.0f, ref = 0.0f;
+  float16_t o[DN], even[2], odd[2];  // scores of the units 0, 2, .. and 1, 3, ..
+#pragma unroll
+  for (int i = 0; i < DN; ++i) o[i] = float16_t{};
+
+  // operand k of the scores of a unit (channels 16 (k >> 1) .., tokens 32 (k &
+  // 1) ..), and of the second product (tile k / DN of 16 tokens, channels 32 (k %
+  // DN) ..)
+  int k_lane = col * D * 2 + ((h ^ swizzle<D>(col)) << 4), v_lane = (2 * h * D + col) * 16;
+  auto key = [&](int kbuf, int k) {
+    return *(const half8_t*)(lds + kbuf * BUF + (k & 1) * 64 * D + (k_lane ^ (k >> 1) << 5));
+  };
+  auto value = [&](int vbuf, int k) {
+    const int te = k / DN;
+    return *(const half8_t*)(lds + (NBK + vbuf) * BUF + v_lane +
+                             ((4 * (te >> 1) + (te & 1)) * D + 32 * (k % DN)) * 16);
+  };
+  // One unit.  EDGE: some row of the wave does not see all of it.
+  auto unit = [&](auto edge, float16_t (&s)[2], float16_t (&next)[2], int u, int kbuf, int vbuf,
+                  int kbuf_in, int vbuf_in) {
+    constexpr bool EDGE = decltype(edge)::value;
+    const int t0 = u * kUnit;
+    // (renewed each unit, so that the compiler forms addresses from these and
+    // does not keep each of them)
+    asm volatile("" : "+v"(k_lane), "+v"(v_lane), "+v"(k_place), "+v"(v_place));
+    float f[NSC], vs[NSC], vs_top;
+#pragma unroll
+    for (int a = 0; a < NSC; ++a) {
+      asm volatile("" : "+v"(ks_next[a]), "+v"(vs_next[a]));
+      // past the sequence's end it may be no page of this sequence
+      const bool held = WHOLE || t0 + 32 * a + 16 * h < seq.len;
+      f[a] = held ? f_row * ks_next[a] : 0.0f;
+      vs[a] = held ? vs_next[a] : 0.0f;
+      if (f[a] == 0.0f) f[a] = 1e-37f;  // a hidden key stays at -inf
+    }
+    vs_top = vs[0];
+    if constexpr (!WHOLE) vs_top = both_halves_max(fmaxf(vs[0], vs[1]));
+    // ---- the rows' maxima
+    float mx = -INFINITY;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      if (EDGE) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (t0 + 32 * a + 16 * h + i >= lim) s[a][i] = -INFINITY;
+      }
+      float t = fmaxf(s[a][0], s[a][1]);
+#pragma unroll
+      for (int i = 2; i < 16; i += 2) t = fmaxf(fmaxf(t, s[a][i]), s[a][i + 1]);
+      mx = fmaxf(mx, t * f[WHOLE ? 0 : a]);
+    }
+    mx = both_halves_max(mx);
+    float back = 1.0f;
+    if (vs_top > 16.0f * ref) {
+      back = ref / vs_top;
+      ref = vs_top;
+    }
+    if (__any(mx > m + 8.0f) || back != 1.0f) {
+      const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= alpha;
+      const float both = alpha * back;
+#pragma unroll
+      for (int i = 0; i < DN; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] *= both;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // ---- the next unit's scores, one product at a time, and between them this
+    // unit's probabilities: operand e of tile a is tokens 16 h + 8 e ..
+    half8_t pf[2][2], fr[4];
+    const float over = ref > 0.0f ? __builtin_amdgcn_rcpf(ref) : 0.0f;
+    float ratio[NSC], shift[NSC], sum[NSC];
+#pragma unroll
+    for (int a = 0; a < NSC; ++a) {
+      const float q_v = vs[a] * over;
+      ratio[a] = q_v < 0x1p-30f ? 0x1p-30f : q_v;
+      shift[a] = __builtin_amdgcn_logf(ratio[a]) - m;
+      sum[a] = 0.0f;
+    }
+    constexpr int N1 = 2 * KS, PER = 32 / N1;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) fr[k] = key(kbuf, k);
+    half8_t qr[2] = {query(0), query(0)};
+#pragma unroll
+    for (int k = 0; k < N1; ++k) {
+      if (k + 3 < N1) fr[(k + 3) & 3] = key(kbuf, k + 3);
+      if ((k & 1) == 0 && k + 2 < N1) qr[(k >> 1) + 1 & 1] = query((k >> 1) + 1);
+      next[k & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[k & 3], qr[k >> 1 & 1], k < 2 ? float16_t{} : next[k & 1],
+                                                           0, 0, 0);
+#pragma unroll
+      for (int x = k * PER; x < (k + 1) * PER; ++x) {
+        const int a = x >> 4, i = x & 15, z = WHOLE ? 0 : a;
+        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], f[z], shift[z]));
+        // exactly 0 where hidden, whatever the page's scales are
+        if (EDGE && t0 + 32 * a + 16 * h + i >= lim) p = 0.0f;
+        sum[z] += p;
+        pf[a][i >> 3][i & 7] = (_Float16)p;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // ---- the second product, and between its steps the staging of the unit
+    // after the next
+    constexpr int N2 = 4 * DN, PARTS = 4 * CH;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) fr[k] = value(vbuf, k);
+#pragma unroll
+    for (int a = 0; a < NSC; ++a)
+      l = sum[a] != 0.0f ? __builtin_fmaf(sum[a], __builtin_amdgcn_rcpf(ratio[a]), l) : l;
+#pragma unroll
+    for (int k = 0; k < N2; ++k) {
+      if (k + 3 < N2) fr[(k + 3) & 3] = value(vbuf, k + 3);
+      o[k % DN] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[k & 3], pf[k / DN >> 1][k / DN & 1],
+                                                         o[k % DN], 0, 0, 0);
+#pragma unroll
+      for (int j = k * PARTS / N2; j < (k + 1) * PARTS / N2; ++j) stage(j, kbuf_in, vbuf_in);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    fetch_scales();
+    fetch(u + 3);
+    turn_pages(u + 4, u + 2);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // ---- the first units
+  if (u0 < u1) {
+    turn_pages(u0, u0);
+    fetch(u0);
+    fetch_scales();
+    turn_pages(u0 + 1, u0 + 1);
+#pragma unroll
+    for (int j = 0; j < 4 * CH; ++j) stage(j, 0, 0);
+    fetch(u0 + 1);
+    turn_pages(u0 + 2, u0 + 1);
+#pragma unroll
+    for (int j = 0; j < 4 * CH; ++j) stage(j, 1, 1);
+    fetch(u0 + 2);
+    turn_pages(u0 + 3, u0 + 1);
+    __syncthreads();
+    even[0] = even[1] = float16_t{};
+#pragma unroll
+    for (int k = 0; k < 2 * KS; ++k)
+      even[k & 1] =
+          __builtin_amdgcn_mfma_f32_32x32x16_f16(key(0, k), query(k >> 1), even[k & 1], 0, 0, 0);
+  }
+  int vb = 0;
+  auto turn = [&](auto edge, float16_t (&now)[2], float16_t (&next)[2], int u, int parity) {
+    if (u > u0) {
+      // the keys of u + 1 and the values of u are whole in LDS, and nobody
+      // reads any more what this iteration overwrites
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    const int vb2 = vb == 0 ? 2 : vb - 1;  // (vb + 2) % 3
+    unit(edge, now, next, u, parity ^ 1, vb, parity, vb2);
+    vb = vb == 2 ? 0 : vb + 1;
+  };
+  int u = u0;
+  for (; u + 1 < u1 && (u + 2) * kUnit <= lim_all; u += 2) {
+    turn(std::false_type{}, even, odd, u, 0);
+    turn(std::false_type{}, odd, even, u + 1, 1);
+  }
+  for (; u < u1; u += 2) {
+    turn(std::true_type{}, even, odd, u, 0);
+    if (u + 1 < u1) turn(std::true_type{}, odd, even, u + 1, 1);
+  }
+  l += __shfl_xor(l, 32, 64);
+
+  // ---- results: register j of o[i] is channel 32 i + (j & 3) + 8 (j >> 2) + 4 h
+  if (!rv) return;
+  if (splits > 1) {
+    const int64_t at_p = ((int64_t)tok * c.H + head) * splits + split;
+#pragma unroll
+    for (int i = 0; i < DN; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4_t v = {o[i][4 * j] * ref, o[i][4 * j + 1] * ref, o[i][4 * j + 2] * ref,
+                            o[i][4 * j + 3] * ref};
+        *(float4_t*)(parts.o + at_p * D + 32 * i + 8 * j + 4 * h) = v;
+      }
+    if (h == 0) {
+      parts.ml[at_p * 2] = m;
+      parts.ml[at_p * 2 + 1] = l;
+    }
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : ref / l;  // a row that sees nothing is 0
+  uint16_t* dst = out + (int64_t)tok * out_stride + head * D;
+#pragma unroll
+  for (int i = 0; i < DN; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = round16<DT>(o[i][4 * j + e] * inv);
+      *(u32x2_t*)(dst + 32 * i + 8 * j + 4 * h) = u32x2_t{y[0] | y[1] << 16, y[2] | y[3] << 16};
+    }
+  if (lse && h == 0)
+    lse[(int64_t)tok * c.H + head] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
 // Joins the splits of a row, in their order: one wave per (token, head).
 template <int DT, int D>
 __global__ void __launch_bounds__(256)
 kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_stride,
-                float* __restrict__ lse, Parts parts, int splits, int units, int max_new) {
+                float* __restrict__ lse, Parts parts, int splits, int units, int rows, int max_new) {
   const int lane = threadIdx.x & 63;
   const int G = c.H / c.Hkv;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -264,7 +655,7 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
   const int hd = (int)(i % c.H), j = (int)(i / c.H % max_new), b = (int)(i / c.H / max_new);
   const Kv8Seq seq = kv8_seq(c, b);
   if (j >= seq.n) return;
-  const int top = tile_limit(seq, causal, (j * G + hd % G) / 16, G);
+  const int top = tile_limit(seq, causal, (j * G + hd % G) / rows, rows, G);
   const int nu = (top + kUnit - 1) / kUnit;
   const int n = clamp_int((nu + units - 1) / units, 1, splits);
   const int64_t row = (int64_t)(seq.tok + j) * c.H + hd;
@@ -287,18 +678,23 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
   if (lse && lane == 0) lse[row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
+// waves: of the prompt kernel's workgroups (32 rows each); 0: the decode kernel.
 struct Plan {
-  int row_tiles, splits, units;
+  int waves, rows, row_tiles, splits, units;
 };
 
-// Splits of the keys: enough workgroups to fill 256 CUs twice, no split below
-// 4 units (one per wave).
-Plan plan_attention(int64_t B, int64_t max_new, int64_t max_len, int H, int Hkv) {
+// Up to 16 rows of a kv head go to the decode kernel, more to the prompt
+// kernel.  Splits of the keys: enough workgroups to fill 256 CUs (four times
+// with the decode kernel's), no split below 4 units.
+Plan plan_attention(int64_t B, int64_t max_new, int64_t max_len, int H, int Hkv, int D) {
   Plan p;
-  p.row_tiles = (int)ceil_div(max_new * (H / Hkv), 16);
+  const int64_t rows = max_new * (H / Hkv);
+  p.waves = rows <= 16 ? 0 : rows <= 64 ? 2 : rows <= 128 || D == 64 ? 4 : 8;
+  p.rows = p.waves ? 32 * p.waves : 16;
+  p.row_tiles = (int)ceil_div(rows, p.rows);
   const int64_t nu = std::max<int64_t>(1, ceil_div(max_len, kUnit));
   const int64_t groups = B * Hkv * p.row_tiles;
-  const int64_t want = std::max<int64_t>(1, ceil_div(1024, groups));
+  const int64_t want = std::max<int64_t>(1, ceil_div(p.waves ? 512 : 1024, groups));
   p.units = (int)std::max<int64_t>(4, ceil_div(nu, want));
   p.splits = (int)ceil_div(nu, p.units);
   return p;
@@ -318,14 +714,26 @@ hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t 
                             int64_t max_new, void* ws, hipStream_t st) {
   Parts parts = {(float*)ws, nullptr};
   parts.ml = parts.o + pad256((int64_t)c.tokens * c.H * p.splits * D * 4) / 4;
-  const int64_t grid = (int64_t)c.B * c.Hkv * p.row_tiles * p.splits;
-  launch_timed(kv8_decode_kernel<DT, D>, dim3((unsigned)grid), dim3(256), 0, st, c,
-               (const uint16_t*)q, q_stride, scale, causal, (uint16_t*)out, out_stride, lse,
-               parts, p.row_tiles, p.splits, p.units);
+  const int64_t groups = (int64_t)c.B * c.Hkv * p.splits;
+  auto go = [&](auto kernel, int64_t grid, int threads) {
+    launch_timed(kernel, dim3((unsigned)grid), dim3(threads), 0, st, c, (const uint16_t*)q,
+                 q_stride, scale, causal, (uint16_t*)out, out_stride, lse, parts, p.row_tiles,
+                 p.splits, p.units);
+  };
+  const int64_t grid = 8 * ceil_div(groups, 8) * p.row_tiles;
+  constexpr int MOST = D == 64 ? 4 : 8;
+  const bool whole = (1 << c.lgT) >= kUnit;
+  if (p.waves == 0) go(kv8_decode_kernel<DT, D>, groups * p.row_tiles, 256);
+  else if (p.waves == 2 && whole) go(kv8_prompt_kernel<DT, D, 2, true>, grid, 128);
+  else if (p.waves == 2) go(kv8_prompt_kernel<DT, D, 2, false>, grid, 128);
+  else if (p.waves == 4 && whole) go(kv8_prompt_kernel<DT, D, 4, true>, grid, 256);
+  else if (p.waves == 4) go(kv8_prompt_kernel<DT, D, 4, false>, grid, 256);
+  else if (whole) go(kv8_prompt_kernel<DT, D, MOST, true>, grid, 64 * MOST);
+  else go(kv8_prompt_kernel<DT, D, MOST, false>, grid, 64 * MOST);
   if (p.splits > 1)
     hipLaunchKernelGGL((kv8_join_kernel<DT, D>),
                        dim3((unsigned)ceil_div((int64_t)c.B * max_new * c.H, 4)), dim3(256), 0,
-                       st, c, causal, (uint16_t*)out, out_stride, lse, parts, p.splits, p.units,
+                       st, c, causal, (uint16_t*)out, out_stride, lse, parts, p.splits, p.units, p.rows,
                        (int)max_new);
   return hipGetLastError();
 }
@@ -343,7 +751,7 @@ int64_t kv8_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t max_new
       max_len > ((int64_t)1 << 30))
     return -1;
   if (tokens == 0 || B == 0 || max_new == 0) return 0;
-  return part_bytes(plan_attention(B, max_new, max_len, H, Hkv), tokens, H, D);
+  return part_bytes(plan_attention(B, max_new, max_len, H, Hkv, D), tokens, H, D);
 }
 
 int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
@@ -366,10 +774,10 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
       return s;
     for (const void* p : {(const void*)cu_seqlens, (const void*)lse, (const void*)workspace})
       if (!aligned16(p)) return W4A16_ERR_MISALIGNED;
-    const Plan p = plan_attention(B, max_new, max_len, H, Hkv);
+    const Plan p = plan_attention(B, max_new, max_len, H, Hkv, D);
     const int64_t need = part_bytes(p, tokens, H, D);
     if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
-    if (B * Hkv * p.row_tiles * p.splits > ((int64_t)1 << 31) - 1 ||
+    if (8 * ceil_div(B * Hkv * p.splits, 8) * p.row_tiles > ((int64_t)1 << 31) - 1 ||
         B * max_new * H > ((int64_t)1 << 32))
       return W4A16_ERR_UNSUPPORTED;
     clear_pending_error();

@@ -326,6 +326,26 @@ def test_nonfinite_queries_and_pages_reach_their_own_rows_alone():
     assert torch.equal(out[0], base[0]) and torch.equal(out[1, :4], base[1, :4])
 
 
+@pytest.mark.parametrize("news", [6, 70])
+def test_pages_ahead_of_a_query_do_not_reach_it(news):
+    """The scales of the pages that only later tokens of a call see are NaN:
+    the earlier tokens' results stay as they are."""
+    T, L = 16, 128 + news
+    c = _case(14, [L], [news], 8, 2, 64, T, "f16")
+    args = (c["cache"], c["dev"]["table"], c["dev"]["lens"])
+    base = w4.kv8_attention(c["q"], *args, cu_seqlens=c["dev"]["cu"])
+    last = int(c["table"][0][(L - 1) // T])
+    first = ((L - 1) // T) * T - (L - news)              # first new token that sees the last page
+    for name in ("k_scale", "v_scale"):
+        keep = c["cache"][name][last].clone()
+        c["cache"][name][last] = float("nan")
+        out = w4.kv8_attention(c["q"], *args, cu_seqlens=c["dev"]["cu"])
+        c["cache"][name][last] = keep
+        if first > 0:
+            assert torch.equal(out[:first], base[:first]), name
+        assert torch.isnan(out[max(first, 0):]).all(), name
+
+
 def test_strides_streams_and_bounds():
     lens, news = [200, 90], [20, 30]
     c = _case(10, lens, news, 8, 2, 64, 64, "f16")
