@@ -368,15 +368,16 @@ def nf4_dequant(nf4, dtype=torch.bfloat16, stream=None):
 _WS = {}
 
 
-def _ws_cache(device, nbytes, stream=None):
+def _ws_cache(device, nbytes, stream=None, kept=None):
+    kept = _WS if kept is None else kept
     key = (device, _stream(stream))
-    cur = _WS.get(key)
+    cur = kept.get(key)
     if cur is None or cur.numel() * 4 < nbytes:
         st = torch.cuda.current_stream() if stream is None else stream
         st.synchronize()
         with torch.cuda.stream(st):     # a block of the stream that uses it
             cur = workspace(max(nbytes, 1 << 20), device)
-        _WS[key] = cur
+        kept[key] = cur
     return cur
 
 

@@ -85,7 +85,7 @@ def load():
 
 
 def lib():
-    return load()
+    return _lib or load()
 
 
 class W4A16Error(RuntimeError):

@@ -21,6 +21,21 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kUnit = 64;  // tokens a wave takes at a time
 
+// The running maximum m of a row (of its scores s in base 2) moves only when a
+// score passes it by kLag, and the reference u that the values' page scales are
+// taken relative to only when one passes twice u.  A probability enters the
+// second product as w = 2^kLift exp2(s - m) (vs / u), at most 2^15 and so in
+// fp16's range, and exact to 2^-11 down to 2^-25 of the largest (2^-36 of it
+// absolutely below that); the sum takes w (u / vs).  vs / u is held to kLeast and
+// up, where every w is 0 in fp16, so that a page of zeros divides nothing by 0.
+// Sums of both products carry the factor 2^kLift, which their quotient drops.
+constexpr float kLift = 11.0f, kLag = 3.0f, kLeast = 0x1p-45f;
+
+// log(sum exp) of a row, natural, from its maximum and sum.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + __log2f(l) - kLift) * kLn2;
+}
+
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
 // 8 codes of two dwords as an fp16 operand: 0x6400 | c is 1024 + c.
@@ -78,11 +93,43 @@ __device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, i
 }
 
 // Partial results of a split: O [row][split][D], then (m, l) [row][split],
-// row = token * H + head.
+// row = token * H + head; and one counter for each (sequence, kv head, row
+// tile) of the decode kernel, 0 between calls.
 struct Parts {
   float* o;
   float* ml;
+  uint32_t* count;
 };
+
+// Two floats past the caches of one die, for a workgroup on another.
+__device__ __forceinline__ void send2(float* to, float a, float b) {
+  const uint64_t v = (uint64_t)__builtin_bit_cast(uint32_t, a) |
+                     (uint64_t)__builtin_bit_cast(uint32_t, b) << 32;
+  __hip_atomic_store((uint64_t*)to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 fetch2(const float* from) {
+  const uint64_t v =
+      __hip_atomic_load((const uint64_t*)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__builtin_bit_cast(float, (uint32_t)v),
+                     __builtin_bit_cast(float, (uint32_t)(v >> 32)));
+}
+
+// The larger of the values that lanes l and l ^ 32 (HALF), or l and l ^ 16
+// hold.  (The swap's results are copied out of their vector before they are
+// reinterpreted: a reinterpreted vector element reads element 0.)
+template <bool HALF>
+__device__ __forceinline__ float swapped_max(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto r = HALF ? __builtin_amdgcn_permlane32_swap(b, b, false, false)
+                      : __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t u = r[0], v = r[1];
+  return fmaxf(__builtin_bit_cast(float, u), __builtin_bit_cast(float, v));
+}
+__device__ __forceinline__ float both_halves_max(float x) { return swapped_max<true>(x); }
+// The largest of the values that the lanes l, l ^ 16, l ^ 32 and l ^ 48 hold.
+__device__ __forceinline__ float four_rows_max(float x) {
+  return swapped_max<true>(swapped_max<false>(x));
+}
 
 // One workgroup of 4 waves per (sequence, kv head, row tile, split of the
 // keys); its waves take units of 64 tokens in turn and are joined in LDS.
@@ -100,18 +147,23 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   __shared__ float stat[4][2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int col = lane & 15, g = lane >> 4;
-  int id = blockIdx.x;
+  // workgroups go to the 8 XCDs in turn: the row tiles of one (split, kv head,
+  // sequence) follow one another on one of them and share its cache
+  const int at_xcd = (int)(blockIdx.x >> 3);
+  int id = at_xcd / row_tiles * 8 + (int)(blockIdx.x & 7);
+  const int rt = at_xcd % row_tiles;
   const int split = id % splits;
   id /= splits;
-  const int rt = id % row_tiles;
-  id /= row_tiles;
   const int hk = id % c.Hkv, b = id / c.Hkv;
+  if (b >= c.B) return;
   const int G = c.H / c.Hkv;
   const Kv8Seq seq = kv8_seq(c, b);
   if (rt * 16 >= seq.n * G) return;
   const int top = tile_limit(seq, causal, rt, 16, G);
   const int nu = (top + kUnit - 1) / kUnit;
-  const int u0 = split * units, u1 = min(u0 + units, nu);
+  // this sequence's units in equal shares, none below `units`
+  const int share = max(units, (nu + splits - 1) / splits);
+  const int u0 = split * share, u1 = min(u0 + share, nu);
   if (split > 0 && u0 >= nu) return;
 
   const int ridx = rt * 16 + col;
@@ -121,7 +173,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
 
   // ---- queries: channels 64 c + 16 g + 8 e .. + 7 of this lane's row
   half8_t qf[DC][2];
-  float rowscale = scale * kLog2e;
+  float f_row = fabsf(scale) * kLog2e;
   {
     const uint16_t* qp = q + (int64_t)tok * q_stride + head * D + 16 * g;
     u32x4_t w[2 * DC];
@@ -129,90 +181,151 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     for (int i = 0; i < 2 * DC; ++i) {
       w[i] = u32x4_t{0, 0, 0, 0};
       if (rv) w[i] = *(const u32x4_t*)(qp + 64 * (i >> 1) + 8 * (i & 1));
+      if (scale < 0.0f) w[i] ^= 0x80008000u;  // the scores' factor is kept positive
     }
     half8_t f[2 * DC];
-    rowscale *= queries_f16<DT, 2 * DC, 16>(w, f);
+    f_row *= queries_f16<DT, 2 * DC, 16>(w, f);
 #pragma unroll
     for (int i = 0; i < 2 * DC; ++i) qf[i >> 1][i & 1] = f[i];
   }
 
-  float m = -INFINITY, l = 0.0f;
+  float m = -1e30f, l = 0.0f, ref = 0.0f;
   float4_t o[DN];
 #pragma unroll
   for (int i = 0; i < DN; ++i) o[i] = float4_t{};
 
+  // ---- a unit's loads: its keys go out as soon as the products have taken the
+  // unit's before, its values likewise, the pages of the unit after ahead of
+  // both.  Lane: keys of the 16 tokens at 16 (col >> 2), values and scales of
+  // those at 16 g.  Units past the last repeat it.
   const int64_t page_bytes = (int64_t)D << c.lgT;
-  auto subtile = [&](int t) -> int64_t {  // of the 16 tokens at t
-    const int page = kv8_page(c, b, min(t >> c.lgT, c.width - 1));
-    return ((int64_t)page * c.Hkv + hk) * page_bytes + (int64_t)(t & ((1 << c.lgT) - 1)) * D;
+  const int32_t* table = c.table + (int64_t)b * c.width;
+  const int last = max(u1 - 1, 0), mask = (1 << c.lgT) - 1;
+  int k_page, v_page;
+  auto turn_pages = [&](int u) {
+    const int t0 = min(u, last) * kUnit;
+    k_page = table[min((t0 + 16 * (col >> 2)) >> c.lgT, c.width - 1)];
+    v_page = table[min((t0 + 16 * g) >> c.lgT, c.width - 1)];
   };
-  for (int u = u0 + wave; u < u1; u += 4) {
-    const int t0 = u * kUnit;
-    const uint8_t* kp = c.k + subtile(t0 + 16 * (col >> 2)) + (col & 3) * D + 16 * g;
-    const uint8_t* vp = c.v + subtile(t0 + 16 * g) + col * 16;
-    const int pg = kv8_page(c, b, min((t0 + 16 * g) >> c.lgT, c.width - 1));
-    const bool held = t0 + 16 * g < seq.len;  // else the page may be no page of this sequence
-    const float ks = held ? c.ks[(int64_t)pg * c.Hkv + hk] : 0.0f;
-    const float vs = held ? c.vs[(int64_t)pg * c.Hkv + hk] : 0.0f;
-    u32x4_t kw[4][DC], vw[DN];
+  u32x4_t kw[4][DC], vw[DN];
+  float ks, vs;
+  auto load_keys = [&](int u) {
+    const int t = min(u, last) * kUnit + 16 * (col >> 2);
+    const uint8_t* from = c.k + ((int64_t)clamp_int(k_page, 0, c.pages - 1) * c.Hkv + hk) * page_bytes +
+                          (t & mask) * D + (col & 3) * D + 16 * g;
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int i = 0; i < DC; ++i) kw[a][i] = *(const u32x4_t*)(kp + a * 4 * D + 64 * i);
+      for (int i = 0; i < DC; ++i) kw[a][i] = *(const u32x4_t*)(from + a * 4 * D + 64 * i);
+  };
+  auto load_values = [&](int u) {
+    const int t = min(u, last) * kUnit + 16 * g;
+    const int64_t slot = (int64_t)clamp_int(v_page, 0, c.pages - 1) * c.Hkv + hk;
+    const uint8_t* from = c.v + slot * page_bytes + (t & mask) * D + col * 16;
+    ks = c.ks[slot];
+    vs = c.vs[slot];
 #pragma unroll
-    for (int i = 0; i < DN; ++i) vw[i] = *(const u32x4_t*)(vp + i * 256);
-
-    float s[4][4], mx = -INFINITY;
-    const float f = rowscale * ks;
+    for (int i = 0; i < DN; ++i) vw[i] = *(const u32x4_t*)(from + i * 256);
+  };
+  if (u0 + wave < u1) {
+    turn_pages(u0 + wave);
+    load_keys(u0 + wave);
+    load_values(u0 + wave);
+    turn_pages(u0 + wave + 4);
+  }
+  // keys that every row of the tile sees
+  const int lim_all = row_limit(seq, causal, rt * 16 / G);
+  const bool whole = c.lgT >= 6;  // a unit lies in one page
+  for (int u = u0 + wave; u < u1; u += 4) {
+    const int t0 = u * kUnit;
+    float4_t s[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      float4_t acc{};
+      s[a] = float4_t{};
 #pragma unroll
       for (int i = 0; i < DC; ++i) {
-        acc = mfma16x16x32<DT_F16>(codes_f16(kw[a][i][0], kw[a][i][1]), qf[i][0], acc);
-        acc = mfma16x16x32<DT_F16>(codes_f16(kw[a][i][2], kw[a][i][3]), qf[i][1], acc);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[a][i] = t0 + 16 * g + 4 * a + i < lim ? acc[i] * f : -INFINITY;
-        mx = fmaxf(mx, s[a][i]);
+        s[a] = mfma16x16x32<DT_F16>(codes_f16(kw[a][i][0], kw[a][i][1]), qf[i][0], s[a]);
+        s[a] = mfma16x16x32<DT_F16>(codes_f16(kw[a][i][2], kw[a][i][3]), qf[i][1], s[a]);
       }
     }
-    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-    const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.0f : mn;
-    const float alpha = __builtin_amdgcn_exp2f(m - ms);
-    m = mn;
-    // the values' scales of the unit's pages, relative to the largest
-    float top_v = fmaxf(vs, __shfl_xor(vs, 16, 64));
-    top_v = fmaxf(top_v, __shfl_xor(top_v, 32, 64));
-    const float rel = top_v > 0.0f ? vs / top_v : (vs == 0.0f ? 1.0f : vs);
+    __builtin_amdgcn_sched_barrier(0);
+    load_keys(u + 4);
+    __builtin_amdgcn_sched_barrier(0);
+    // past the sequence's end it may be no page of this sequence
+    const bool held = whole || t0 + 16 * g < seq.len;
+    float f = held ? f_row * ks : 0.0f;
+    if (f == 0.0f) f = 1e-37f;  // a hidden key stays at -inf
+    const float v_scale = held ? vs : 0.0f;
+    const float vs_top = whole ? v_scale : four_rows_max(v_scale);
+    // rows past the tile's last see what the others do; they are not written
+    const bool edge = t0 + kUnit > lim_all;
+    if (edge) {
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t0 + 16 * g + 4 * a + i >= lim) s[a][i] = -INFINITY;
+    }
+    float mx = fmaxf(s[0][0], s[0][1]);
+#pragma unroll
+    for (int i = 2; i < 16; i += 2) mx = fmaxf(fmaxf(mx, s[i >> 2][i & 3]), s[i >> 2][(i & 3) + 1]);
+    mx = four_rows_max(mx * f);
+    float back = 1.0f;
+    if (vs_top > 2.0f * ref) {
+      back = ref / vs_top;
+      ref = vs_top;
+    }
+    if (__any(mx > m + kLag) || back != 1.0f) {
+      const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= alpha;
+      const float both = alpha * back;
+#pragma unroll
+      for (int i = 0; i < DN; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= both;
+    }
+    const float q_v = v_scale * (ref > 0.0f ? __builtin_amdgcn_rcpf(ref) : 0.0f);
+    const float ratio = q_v < kLeast ? kLeast : q_v;
+    const float shift = __builtin_amdgcn_logf(ratio) + kLift - m;
     half8_t pf[2];
     float sum = 0.0f;
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s[a][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], f, shift));
+    if (edge) {
+      // exactly 0 where hidden, whatever the page's scales are
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t0 + 16 * g + 4 * a + i >= lim) s[a][i] = 0.0f;
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float p = __builtin_amdgcn_exp2f(s[a][i] - ms);
-        sum += p;
-        pf[a >> 1][4 * (a & 1) + i] = (_Float16)(p == 0.0f ? 0.0f : p * rel);
+        sum += s[a][i];
+        pf[a >> 1][4 * (a & 1) + i] = (_Float16)s[a][i];
       }
-    l = l * alpha + sum;
+    l = sum != 0.0f ? __builtin_fmaf(sum, __builtin_amdgcn_rcpf(ratio), l) : l;
 #pragma unroll
     for (int i = 0; i < DN; ++i) {
-      float4_t acc{};
-      acc = mfma16x16x32<DT_F16>(codes_f16(vw[i][0], vw[i][1]), pf[0], acc);
-      acc = mfma16x16x32<DT_F16>(codes_f16(vw[i][2], vw[i][3]), pf[1], acc);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = __builtin_fmaf(acc[j], top_v, o[i][j] * alpha);
+      o[i] = mfma16x16x32<DT_F16>(codes_f16(vw[i][0], vw[i][1]), pf[0], o[i]);
+      o[i] = mfma16x16x32<DT_F16>(codes_f16(vw[i][2], vw[i][3]), pf[1], o[i]);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    load_values(u + 4);
+    turn_pages(u + 8);
   }
   l += __shfl_xor(l, 16, 64);
   l += __shfl_xor(l, 32, 64);
 
   // ---- join the waves: lane holds channels 16 i + 4 g + j of row col
 #pragma unroll
-  for (int i = 0; i < DN; ++i) *(float4_t*)&joined[wave][col][16 * i + 4 * g] = o[i];
+  for (int i = 0; i < DN; ++i) *(float4_t*)&joined[wave][col][16 * i + 4 * g] = o[i] * ref;
   if (g == 0) {
     stat[wave][0][col] = m;
     stat[wave][1][col] = l;
@@ -221,7 +334,6 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   // 16 lanes per row
   const int row = tid >> 4, part = tid & 15;
   const int rr = rt * 16 + row;
-  if (rr >= seq.n * G) return;
   float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
   for (int w = 0; w < 4; ++w) mm = fmaxf(mm, stat[w][0][row]);
@@ -232,39 +344,70 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     wt[w] = __builtin_amdgcn_exp2f(stat[w][0][row] - base);
     ll += wt[w] * stat[w][1][row];
   }
-  constexpr int E = D / 16;  // channels per lane
+  // channels of this lane: pairs 32 apart, so that 16 lanes hold 32 in a row
+  constexpr int E = D / 16;
+  auto channel = [&](int j) { return 32 * (j >> 1) + 2 * part + (j & 1); };
   float r[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) {
     r[j] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) r[j] += wt[w] * joined[w][row][part * E + j];
+    for (int w = 0; w < 4; ++w) r[j] += wt[w] * joined[w][row][channel(j)];
   }
-  const int64_t tk = seq.tok + rr / G;
+  const int64_t tk = seq.tok + min(rr / G, seq.n - 1);
   const int hd = hk * G + rr % G;
-  if (splits > 1) {
-    const int64_t at = (tk * c.H + hd) * splits + split;
+  const int mine = max(1, (nu + share - 1) / share);  // splits with a unit
+  if (mine > 1) {
+    // ---- the last workgroup of the tile to arrive joins the splits, in order.
+    // The partials go through the point where the GPU's caches meet (agent-scope
+    // accesses) and have arrived there before the count does: a fence instead
+    // would write back and empty a whole L2 for each workgroup (MI355X, 64
+    // sequences of 8192 tokens: 490 us with fences).
+    const int64_t at = (tk * c.H + hd) * splits;
+    if (rr < seq.n * G) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) parts.o[at * D + part * E + j] = r[j];
-    if (part == 0) {
-      parts.ml[at * 2] = mm;
-      parts.ml[at * 2 + 1] = ll;
+      for (int j = 0; j < E; j += 2) send2(parts.o + (at + split) * D + channel(j), r[j], r[j + 1]);
+      if (part == 0) send2(parts.ml + (at + split) * 2, mm, ll);
     }
-    return;
+    __shared__ uint32_t arrived;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t* count = parts.count + ((int64_t)b * c.Hkv + hk) * row_tiles + rt;
+      arrived = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (arrived == (uint32_t)mine - 1)  // the last: ready for the next call
+        __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (arrived != (uint32_t)mine - 1 || rr >= seq.n * G) return;
+    mm = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < mine; ++i) mm = fmaxf(mm, fetch2(parts.ml + (at + i) * 2).x);
+    const float from = mm == -INFINITY ? 0.0f : mm;
+    ll = 0.0f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) r[j] = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < mine; ++i) {
+      const float2 s = fetch2(parts.ml + (at + i) * 2);
+      const float w = __builtin_amdgcn_exp2f(s.x - from);
+      ll += w * s.y;
+#pragma unroll
+      for (int j = 0; j < E; j += 2) {
+        const float2 v = fetch2(parts.o + (at + i) * D + channel(j));
+        r[j] += w * v.x;
+        r[j + 1] += w * v.y;
+      }
+    }
   }
+  if (rr >= seq.n * G) return;
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;  // a row that sees nothing is 0
 #pragma unroll
-  for (int j = 0; j < E; ++j)
-    out[tk * out_stride + hd * D + part * E + j] = round16<DT>(r[j] * inv);
+  for (int j = 0; j < E; j += 2)
+    *(uint32_t*)(out + tk * out_stride + hd * D + channel(j)) =
+        (uint32_t)round16<DT>(r[j] * inv) | (uint32_t)round16<DT>(r[j + 1] * inv) << 16;
   if (lse && part == 0)
-    lse[tk * c.H + hd] = ll == 0.0f ? -INFINITY : (mm + __log2f(ll)) * kLn2;
-}
-
-// The larger of the values that lanes l and l ^ 32 hold.
-__device__ __forceinline__ float both_halves_max(float x) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, x);
-  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return fmaxf(__builtin_bit_cast(float, r[0]), __builtin_bit_cast(float, r[1]));
+    lse[tk * c.H + hd] = lse_of(mm, ll);
 }
 
 // Position of a key row's 16-byte chunks in LDS (rows of 2 D bytes): 16 lanes
@@ -288,11 +431,6 @@ __device__ __forceinline__ int swizzle(int row) {
 //    Keys: rows of 2 D bytes, their 16-byte chunks permuted by row; values:
 //    [16 tokens][8 of them][channel] pieces of 16 bytes.  Reads and writes meet
 //    all banks.
-//  * The running maximum m of a row moves only when a score passes it by 2^8
-//    (fp16 holds the probabilities up to then); so does the reference u that
-//    the values' page scales are taken relative to, by 2^4.  A probability
-//    enters the second product as w = exp2(s - m + log2(vs / u)) and the sum as
-//    w (u / vs); vs / u is held to 2^-30 and up, below which w is 0 in fp16.
 //
 // WHOLE: pages of 64 tokens and more, a unit lies in one page.
 template <int DT, int D, int W, bool WHOLE>
@@ -496,11 +634,11 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     }
     mx = both_halves_max(mx);
     float back = 1.0f;
-    if (vs_top > 16.0f * ref) {
+    if (vs_top > 2.0f * ref) {
       back = ref / vs_top;
       ref = vs_top;
     }
-    if (__any(mx > m + 8.0f) || back != 1.0f) {
+    if (__any(mx > m + kLag) || back != 1.0f) {
       const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= alpha;
@@ -519,8 +657,8 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
 #pragma unroll
     for (int a = 0; a < NSC; ++a) {
       const float q_v = vs[a] * over;
-      ratio[a] = q_v < 0x1p-30f ? 0x1p-30f : q_v;
-      shift[a] = __builtin_amdgcn_logf(ratio[a]) - m;
+      ratio[a] = q_v < kLeast ? kLeast : q_v;
+      shift[a] = __builtin_amdgcn_logf(ratio[a]) + kLift - m;
       sum[a] = 0.0f;
     }
     constexpr int N1 = 2 * KS, PER = 32 / N1;
@@ -640,10 +778,11 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       *(u32x2_t*)(dst + 32 * i + 8 * j + 4 * h) = u32x2_t{y[0] | y[1] << 16, y[2] | y[3] << 16};
     }
   if (lse && h == 0)
-    lse[(int64_t)tok * c.H + head] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    lse[(int64_t)tok * c.H + head] = lse_of(m, l);
 }
 
-// Joins the splits of a row, in their order: one wave per (token, head).
+// Joins the prompt kernel's splits of a row, in their order: one wave per
+// (token, head).
 template <int DT, int D>
 __global__ void __launch_bounds__(256)
 kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_stride,
@@ -675,45 +814,55 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
 #pragma unroll
   for (int e = 0; e < E; ++e)
     out[(seq.tok + j) * out_stride + hd * D + lane * E + e] = round16<DT>(r[e] * inv);
-  if (lse && lane == 0) lse[row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+  if (lse && lane == 0) lse[row] = lse_of(m, l);
 }
 
 // waves: of the prompt kernel's workgroups (32 rows each); 0: the decode kernel.
+constexpr int64_t kCounters = 16384;
+
 struct Plan {
   int waves, rows, row_tiles, splits, units;
 };
 
-// Up to 16 rows of a kv head go to the decode kernel, more to the prompt
-// kernel.  Splits of the keys: enough workgroups to fill 256 CUs (four times
-// with the decode kernel's), no split below 4 units.
+// Up to 128 rows of a kv head go to the decode kernel in tiles of 16, which
+// follow one another on one die and find the keys in its cache; more to the
+// prompt kernel (MI355X, 24 sequences of 4001 tokens, 4 kv heads of 64: 40 rows
+// 28 us against 46 in the prompt kernel's form, 128 rows 45 against 53).
+// Splits of the keys: two workgroups for each of 256 CUs in all (64 sequences
+// of 8192 tokens, 8 kv heads of 128: 186 us; with 1024 workgroups 192, with
+// 3072 215), no split below 8 units (two a wave; the prompt kernel's 4).
 Plan plan_attention(int64_t B, int64_t max_new, int64_t max_len, int H, int Hkv, int D) {
   Plan p;
   const int64_t rows = max_new * (H / Hkv);
-  p.waves = rows <= 16 ? 0 : rows <= 64 ? 2 : rows <= 128 || D == 64 ? 4 : 8;
+  p.waves = rows <= 128 ? 0 : D == 64 ? 4 : 8;
   p.rows = p.waves ? 32 * p.waves : 16;
   p.row_tiles = (int)ceil_div(rows, p.rows);
   const int64_t nu = std::max<int64_t>(1, ceil_div(max_len, kUnit));
   const int64_t groups = B * Hkv * p.row_tiles;
-  const int64_t want = std::max<int64_t>(1, ceil_div(p.waves ? 512 : 1024, groups));
-  p.units = (int)std::max<int64_t>(4, ceil_div(nu, want));
-  p.splits = (int)ceil_div(nu, p.units);
+  const int64_t want = std::max<int64_t>(1, ceil_div(512, groups));
+  p.units = (int)(p.waves ? std::max<int64_t>(4, ceil_div(nu, want)) : 8);
+  if (groups > kCounters) p.units = (int)nu;
+  p.splits = (int)std::min(ceil_div(nu, p.units), want);
   return p;
 }
 
 int64_t pad256(int64_t b) { return ceil_div(b, 256) * 256; }
 
+// The workspace begins with the decode kernel's counters, at the same place
+// in every call: they are zero between calls, whatever the calls' sizes.
 int64_t part_bytes(const Plan& p, int64_t tokens, int H, int D) {
   if (p.splits == 1) return 0;
   const int64_t rows = tokens * H * p.splits;
-  return pad256(rows * D * 4) + pad256(rows * 8);
+  return kCounters * 4 + pad256(rows * D * 4) + pad256(rows * 8);
 }
 
 template <int DT, int D>
 hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t q_stride,
                             float scale, int causal, void* out, int64_t out_stride, float* lse,
                             int64_t max_new, void* ws, hipStream_t st) {
-  Parts parts = {(float*)ws, nullptr};
-  parts.ml = parts.o + pad256((int64_t)c.tokens * c.H * p.splits * D * 4) / 4;
+  const int64_t rows = (int64_t)c.tokens * c.H * p.splits;
+  Parts parts = {(float*)((uint8_t*)ws + kCounters * 4), nullptr, (uint32_t*)ws};
+  parts.ml = parts.o + pad256(rows * D * 4) / 4;
   const int64_t groups = (int64_t)c.B * c.Hkv * p.splits;
   auto go = [&](auto kernel, int64_t grid, int threads) {
     launch_timed(kernel, dim3((unsigned)grid), dim3(threads), 0, st, c, (const uint16_t*)q,
@@ -721,16 +870,12 @@ hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t 
                  p.splits, p.units);
   };
   const int64_t grid = 8 * ceil_div(groups, 8) * p.row_tiles;
-  constexpr int MOST = D == 64 ? 4 : 8;
+  constexpr int WAVES = D == 64 ? 4 : 8;
   const bool whole = (1 << c.lgT) >= kUnit;
-  if (p.waves == 0) go(kv8_decode_kernel<DT, D>, groups * p.row_tiles, 256);
-  else if (p.waves == 2 && whole) go(kv8_prompt_kernel<DT, D, 2, true>, grid, 128);
-  else if (p.waves == 2) go(kv8_prompt_kernel<DT, D, 2, false>, grid, 128);
-  else if (p.waves == 4 && whole) go(kv8_prompt_kernel<DT, D, 4, true>, grid, 256);
-  else if (p.waves == 4) go(kv8_prompt_kernel<DT, D, 4, false>, grid, 256);
-  else if (whole) go(kv8_prompt_kernel<DT, D, MOST, true>, grid, 64 * MOST);
-  else go(kv8_prompt_kernel<DT, D, MOST, false>, grid, 64 * MOST);
-  if (p.splits > 1)
+  if (p.waves == 0) go(kv8_decode_kernel<DT, D>, grid, 256);
+  else if (whole) go(kv8_prompt_kernel<DT, D, WAVES, true>, grid, 64 * WAVES);
+  else go(kv8_prompt_kernel<DT, D, WAVES, false>, grid, 64 * WAVES);
+  if (p.waves && p.splits > 1)
     hipLaunchKernelGGL((kv8_join_kernel<DT, D>),
                        dim3((unsigned)ceil_div((int64_t)c.B * max_new * c.H, 4)), dim3(256), 0,
                        st, c, causal, (uint16_t*)out, out_stride, lse, parts, p.splits, p.units, p.rows,

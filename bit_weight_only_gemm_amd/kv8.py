@@ -10,6 +10,8 @@ page_table int32 [B, max_pages], seq_lens int32 [B] (the new tokens included)
 and cu_seqlens int32 [B + 1] stay on the device; without cu_seqlens each
 sequence has one new token.  Rows of q, k and v are [tokens, heads, D] and may
 be slices of a fused projection.
+
+(A decode step's calls are short: the checks below look at each tensor once.)
 """
 
 import math
@@ -17,7 +19,12 @@ import math
 import torch
 
 from . import _DT, _lib, _need, _stream
-from .w8a8 import _at, _empty, _space
+from .w8a8 import _empty, _space
+
+
+# Workspaces of kv8_attention by (device, stream): it keeps counters in them,
+# zero between calls, so no other operator writes there.
+_COUNTED = {}
 
 
 def kv8_cache(num_pages, page_size, kv_heads, head_dim, device="cuda"):
@@ -35,16 +42,19 @@ def kv8_cache(num_pages, page_size, kv_heads, head_dim, device="cuda"):
 
 
 def _cache(c):
+    """The cache's sizes and the addresses of its arrays."""
     pages, Hkv, T, D = c["num_pages"], c["kv_heads"], c["page_size"], c["head_dim"]
-    _need(c["k"], torch.uint8, "cache k", pages * Hkv * T * D)
-    _need(c["v"], torch.uint8, "cache v", pages * Hkv * T * D)
-    _need(c["k_scale"], torch.float32, "cache k_scale", pages * Hkv)
-    _need(c["v_scale"], torch.float32, "cache v_scale", pages * Hkv)
-    return pages, Hkv, T, D
+    k, v, ks, vs = c["k"], c["v"], c["k_scale"], c["v_scale"]
+    _need(k, torch.uint8, "cache k", pages * Hkv * T * D)
+    _need(v, torch.uint8, "cache v", pages * Hkv * T * D)
+    _need(ks, torch.float32, "cache k_scale", pages * Hkv)
+    _need(vs, torch.float32, "cache v_scale", pages * Hkv)
+    return pages, Hkv, T, D, (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
 
 
 def _heads(t, dtype, name, tokens=None, heads=None, D=None):
-    """Checks rows [tokens, heads, D], contiguous within a token; the row stride."""
+    """Checks rows [tokens, heads, D], contiguous within a token; (tokens,
+    heads, row stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if t.dtype not in _DT or (dtype is not None and t.dtype != dtype):
@@ -55,10 +65,12 @@ def _heads(t, dtype, name, tokens=None, heads=None, D=None):
     if d != D or (tokens is not None and n != tokens) or (heads is not None and h != heads):
         raise ValueError("%s has shape %s, expected [%s, %s, %d]"
                          % (name, tuple(t.shape), tokens or "tokens", heads or "heads", D))
+    if t.is_contiguous():
+        return n, h, h * D
     step, head, one = t.stride()
     if n and (one != 1 or (h > 1 and head != D)):
         raise ValueError("%s must be contiguous within a token" % name)
-    return step if n > 1 else h * D
+    return n, h, step if n > 1 else h * D
 
 
 def _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens):
@@ -70,9 +82,9 @@ def _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens):
     if cu_seqlens is None:
         if tokens != B:
             raise ValueError("%d tokens for %d sequences: pass cu_seqlens" % (tokens, B))
-        return B, width, 1 if B else 0
+        return B, width, 1 if B else 0, None
     _need(cu_seqlens, torch.int32, "cu_seqlens", B + 1)
-    return B, width, tokens if max_new is None else min(int(max_new), tokens)
+    return B, width, tokens if max_new is None else min(int(max_new), tokens), cu_seqlens.data_ptr()
 
 
 def kv8_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, max_new=None, q=None,
@@ -81,21 +93,24 @@ def kv8_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, max_new=None,
     positions (cos, sin fp32 [positions, rope_dim / 2]), and returns the
     rotated queries q [tokens, H, D] (None without q).  max_new: an upper bound
     of the new tokens of one sequence (all of them when not given)."""
-    pages, Hkv, T, D = _cache(cache)
-    k_stride = _heads(k, None, "k", None, Hkv, D)
-    tokens = k.shape[0]
-    v_stride = _heads(v, k.dtype, "v", tokens, Hkv, D)
-    B, width, max_new = _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens)
-    H, q_stride, o_stride = Hkv, 0, 0
+    pages, Hkv, T, D, arrays = _cache(cache)
+    tokens, _, k_stride = _heads(k, None, "k", None, Hkv, D)
+    dtype = k.dtype
+    _, _, v_stride = _heads(v, dtype, "v", tokens, Hkv, D)
+    B, width, max_new, cu = _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens)
+    H, q_at, q_stride, o_at, o_stride = Hkv, None, 0, None, 0
     if q is not None:
-        q_stride = _heads(q, k.dtype, "q", tokens, None, D)
-        H = q.shape[1]
+        _, H, q_stride = _heads(q, dtype, "q", tokens, None, D)
         if q_out is None:
-            q_out = _empty((tokens, H, D), q.dtype, q.device, stream)
-        o_stride = _heads(q_out, k.dtype, "q_out", tokens, H, D)
+            q_out = _empty((tokens, H, D), dtype, q.device, stream)
+            o_stride = H * D
+        else:
+            _, _, o_stride = _heads(q_out, dtype, "q_out", tokens, H, D)
+        q_at, o_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     rows = dim = 0
+    cos_at = sin_at = None
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
@@ -103,28 +118,31 @@ def kv8_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, max_new=None,
         _need(sin, torch.float32, "sin", cos.numel())
         if cos.dim() != 2:
             raise ValueError("cos must be [positions, rope_dim / 2]")
-        rows, dim = cos.shape[0], 2 * cos.shape[1]
-    _lib.check(_lib.lib().kv8_append(
-        _at(q), q_stride, _at(q_out), o_stride, _at(k), k_stride, _at(v), v_stride,
-        _at(cache["k"]), _at(cache["v"]), _at(cache["k_scale"]), _at(cache["v_scale"]), pages,
-        T, _at(page_table), width, _at(seq_lens), _at(cu_seqlens), _at(cos), _at(sin), rows,
-        dim, int(interleaved), tokens, B, max_new, H, Hkv, D, _DT[k.dtype], _stream(stream)),
-        "kv8_append")
+        rows, dim = cos.shape
+        dim *= 2
+        cos_at, sin_at = cos.data_ptr(), sin.data_ptr()
+    status = _lib.lib().kv8_append(
+        q_at, q_stride, o_at, o_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, *arrays,
+        pages, T, page_table.data_ptr(), width, seq_lens.data_ptr(), cu, cos_at, sin_at, rows, dim,
+        1 if interleaved else 0, tokens, B, max_new, H, Hkv, D, _DT[dtype], _stream(stream))
+    if status:
+        _lib.check(status, "kv8_append")
     return q_out
 
 
 def kv8_dequant(cache, pages, dtype=torch.bfloat16, stream=None):
     """The values of pages (int32 [n]) of the cache: k, v [n, Hkv, T, D]."""
-    num, Hkv, T, D = _cache(cache)
+    num, Hkv, T, D, arrays = _cache(cache)
     if dtype not in _DT:
         raise TypeError("dtype must be float16 or bfloat16")
     _need(pages, torch.int32, "pages")
     n = pages.numel()
-    k = _empty((n, Hkv, T, D), dtype, pages.device, stream)
-    v = _empty((n, Hkv, T, D), dtype, pages.device, stream)
-    _lib.check(_lib.lib().kv8_dequant(
-        _at(cache["k"]), _at(cache["v"]), _at(cache["k_scale"]), _at(cache["v_scale"]), num, T,
-        Hkv, D, _at(pages), n, _DT[dtype], _at(k), _at(v), _stream(stream)), "kv8_dequant")
+    shape, device = (n, Hkv, T, D), pages.device
+    k, v = _empty(shape, dtype, device, stream), _empty(shape, dtype, device, stream)
+    status = _lib.lib().kv8_dequant(*arrays, num, T, Hkv, D, pages.data_ptr(), n, _DT[dtype],
+                                    k.data_ptr(), v.data_ptr(), _stream(stream))
+    if status:
+        _lib.check(status, "kv8_dequant")
     return k, v
 
 
@@ -142,23 +160,27 @@ def kv8_attention(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
     [tokens, H, D] in q's dtype.  scale: 1 / sqrt(D) when not given; max_new,
     max_len: upper bounds of the new tokens and of the length of one sequence
     (all tokens, the table's width); lse: fp32 [tokens, H], written if given."""
-    pages, Hkv, T, D = _cache(cache)
-    q_stride = _heads(q, None, "q", None, None, D)
-    tokens, H = q.shape[0], q.shape[1]
-    B, width, max_new = _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens)
+    pages, Hkv, T, D, arrays = _cache(cache)
+    tokens, H, q_stride = _heads(q, None, "q", None, None, D)
+    dtype = q.dtype
+    B, width, max_new, cu = _sequences(page_table, seq_lens, cu_seqlens, max_new, tokens)
     max_len = width * T if max_len is None else min(int(max_len), width * T)
     if out is None:
-        out = _empty((tokens, H, D), q.dtype, q.device, stream)
-    o_stride = _heads(out, q.dtype, "out", tokens, H, D)
+        out = _empty((tokens, H, D), dtype, q.device, stream)
+        o_stride = H * D
+    else:
+        _, _, o_stride = _heads(out, dtype, "out", tokens, H, D)
     if lse is not None:
         _need(lse, torch.float32, "lse", tokens * H)
     L = _lib.lib()
-    need = max(0, int(L.kv8_attention_workspace_bytes(tokens, B, max_new, max_len, H, Hkv, D)))
-    workspace, nbytes = _space(workspace, need, q.device, stream)
-    _lib.check(L.kv8_attention(
-        _at(q), q_stride, _at(cache["k"]), _at(cache["v"]), _at(cache["k_scale"]),
-        _at(cache["v_scale"]), pages, T, _at(page_table), width, _at(seq_lens),
-        _at(cu_seqlens), 1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
-        _at(out), o_stride, _at(lse), tokens, B, max_new, max_len, H, Hkv, D, _DT[q.dtype],
-        _at(workspace), nbytes, _stream(stream)), "kv8_attention")
+    need = L.kv8_attention_workspace_bytes(tokens, B, max_new, max_len, H, Hkv, D)
+    workspace, nbytes = _space(workspace, need, q.device, stream, _COUNTED)
+    status = L.kv8_attention(
+        q.data_ptr(), q_stride, *arrays, pages, T, page_table.data_ptr(), width,
+        seq_lens.data_ptr(), cu, 1.0 / math.sqrt(D) if scale is None else float(scale),
+        1 if causal else 0, out.data_ptr(), o_stride, None if lse is None else lse.data_ptr(),
+        tokens, B, max_new, max_len, H, Hkv, D, _DT[dtype],
+        None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream))
+    if status:
+        _lib.check(status, "kv8_attention")
     return out

@@ -95,9 +95,9 @@ def _output(out, shape, dtype, device, stream):
     return out
 
 
-def _space(workspace, need, device, stream):
+def _space(workspace, need, device, stream, kept=None):
     if workspace is None and need > 0:
-        workspace = _ws_cache(device, need, stream)
+        workspace = _ws_cache(device, need, stream, kept)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return workspace, nbytes
 
@@ -130,12 +130,15 @@ def w8a8_gemm(xq, x_scale, wq, w_scale, bias=None, dtype=torch.bfloat16, out=Non
 def w8a8_linear(x, wq, w_scale, bias=None, out=None, workspace=None, stream=None):
     """y = x @ (wq * w_scale)^T + bias for x [..., K] fp16/bf16, quantized per
     row on the way (w8a8_quantize and w8a8_gemm in one call)."""
-    M, K, stride = _rows(x, tuple(_DT), "x", wq.shape[-1])
-    N, _ = _weights(wq, w_scale, bias, x.dtype)
-    out = _output(out, (*x.shape[:-1], N), x.dtype, x.device, stream)
-    need = max(0, int(_lib.lib().w8a8_workspace_bytes(M, N, K, 1)))
-    workspace, nbytes = _space(workspace, need, x.device, stream)
-    _lib.check(_lib.lib().w8a8_linear(_at(x), stride, _at(wq), _at(w_scale), _at(bias),
-                                      _at(out), M, N, K, _DT[x.dtype], _at(workspace), nbytes,
-                                      _stream(stream)), "w8a8_linear")
+    N, K = _weights(wq, w_scale, bias, x.dtype)
+    M, _, stride = _rows(x, _DT, "x", K)
+    dtype = x.dtype
+    out = _output(out, (*x.shape[:-1], N), dtype, x.device, stream)
+    L = _lib.lib()
+    workspace, nbytes = _space(workspace, L.w8a8_workspace_bytes(M, N, K, 1), x.device, stream)
+    status = L.w8a8_linear(x.data_ptr(), stride, wq.data_ptr(), w_scale.data_ptr(), _at(bias),
+                           out.data_ptr(), M, N, K, _DT[dtype], _at(workspace), nbytes,
+                           _stream(stream))
+    if status:
+        _lib.check(status, "w8a8_linear")
     return out

@@ -622,7 +622,9 @@ int64_t kv8_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t max_new
  *             split of the keys is planned; longer sequences are cut to
  *             the planned units.
  *   workspace required where kv8_attention_workspace_bytes is not 0
- *             (W4A16_ERR_WORKSPACE when NULL or smaller).
+ *             (W4A16_ERR_WORKSPACE when NULL or smaller).  Filled with zeros
+ *             before its first use and used by kv8_attention alone: it holds
+ *             counters that every call leaves at zero.
  * Async.  Bitwise reproducible (splits are joined in order).
  */
 int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,

@@ -291,6 +291,29 @@ def test_queries_of_any_magnitude(scale_q):
     _check_attention(c, 4, 2, 128, "bf16", one=True, scale=0.1 / scale_q)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [1.7, -1.7])
+@pytest.mark.parametrize("news", [[1, 1], [5, 9], [200, 150]])
+@pytest.mark.parametrize("D,T", [(64, 16), (128, 64)])
+def test_scores_far_apart(D, T, news, scale, dtype):
+    """Scores of hundreds, the largest anywhere in a unit: what fp16 could not
+    hold if the running maximum missed a token.  Beside the relative bound a
+    probability below fp16's normal range is off by 2^-25 where the largest is
+    2^11 and up, 2^-36, in each of the seen tokens of up to 128 codes."""
+    lens = [260, 333]
+    c = _case(15, lens, news, 8, 2, D, T, dtype)
+    out = w4.kv8_attention(c["q"], c["cache"], c["dev"]["table"], c["dev"]["lens"],
+                           cu_seqlens=c["dev"]["cu"], scale=scale, max_new=max(news))
+    n = _np(c)
+    k = n["k"] * n["ks"].astype(np.float64)[:, :, None, None]
+    v = n["v"] * n["vs"].astype(np.float64)[:, :, None, None]
+    want, mass, _, work = kv8.attention(c["q"].float().cpu().numpy(), k, v, c["table"], lens,
+                                        c["cu"], T, scale, True)
+    bound, _ = kv8.attention_bounds(want, mass, work, max(lens), D, dtype)
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert np.all(err <= bound + max(lens) * 128 * 2.0 ** -36 * n["vs"].max())
+
+
 @pytest.mark.parametrize("news", [[1, 1], [5, 9], [90, 70]])
 def test_masked_places_do_not_matter(news):
     """NaN scales and any codes in pages of no sequence, and rows past a
