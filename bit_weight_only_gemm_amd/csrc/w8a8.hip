@@ -22,10 +22,17 @@ typedef int i32x16_t __attribute__((ext_vector_type(16)));
 namespace {
 
 // ------------------------------------------------------------- quantizer ---
-// One workgroup per row; a row that fits 256 lanes x 8 x kHold values is read
-// once and kept in registers between its maximum and its codes, a longer one
-// is read again (from cache).
-constexpr int kHold = 8;
+// One workgroup of LANES lanes per row.  The first 16384 values are read once,
+// every load out before the first is used, and kept in registers between the
+// row's maximum and its codes; what a longer row has beyond them is read again
+// (from cache).
+//
+// The bytes bound it where there are many rows (8192 x 5120 in bf16: 29 us,
+// 4.3 TB/s), a row's chain of load, maximum, division and store where there are
+// few: then 1024 lanes share that chain (MI355X, 256 lanes -> 1024: 16 x 11008
+// 5.0 -> 4.5 us, 512 x 11008 7.9 -> 7.3, but 1024 x 4096 6.4 -> 7.5 and 8192 x
+// 5120 29 -> 47, where the barriers of large workgroups show).
+constexpr int kHeld = 16384, kFewRows = 512 + 1;
 
 template <int DT>
 __device__ __forceinline__ void load8(const void* x, int64_t i, float (&f)[8]) {
@@ -48,26 +55,44 @@ __device__ __forceinline__ u32x2_t codes8(const float (&f)[8], const Codes8& q) 
   return r;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256)
+template <int DT, int LANES>
+__global__ void __launch_bounds__(LANES)
 w8a8_quantize_kernel(const void* __restrict__ x, int64_t stride, int K, int8_t* __restrict__ codes,
                      float* __restrict__ scales) {
-  __shared__ uint32_t part[4];
+  constexpr int HOLD = kHeld / (8 * LANES), BYTES = DT == 2 ? 4 : 2, PARTS = BYTES / 2;
+  __shared__ uint32_t part[LANES / 64];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
   const int64_t base = row * stride;
-  float f[kHold][8];
+  // (a load past the row's end gives zeros)
+  const rsrc_t r = make_rsrc((const uint8_t*)x + base * BYTES, (uint32_t)K * BYTES);
+  u32x4_t raw[HOLD][PARTS];
+#pragma unroll
+  for (int i = 0; i < HOLD; ++i)
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+      raw[i][p] = bld128(r, (uint32_t)(i * LANES + tid) * 8 * BYTES + 16 * p, 0);
+  auto held = [&](int i, float (&f)[8]) {
+    if constexpr (DT == 2) {
+      const u32x4_t lo = raw[i][0], hi = raw[i][PARTS - 1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = lo[j], b = hi[j];
+        f[j] = __builtin_bit_cast(float, a), f[4 + j] = __builtin_bit_cast(float, b);
+      }
+    } else {
+      widen8<DT>(raw[i][0], f);
+    }
+  };
   uint32_t mag = 0;
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) {
-    const int k = (i * 256 + tid) * 8;
-    if (k < K) {
-      load8<DT>(x, base + k, f[i]);
+  for (int i = 0; i < HOLD; ++i) {
+    float f[8];
+    held(i, f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mag = max(mag, mag_bits(f[i][j]));
-    }
+    for (int j = 0; j < 8; ++j) mag = max(mag, mag_bits(f[j]));
   }
-  for (int k = (kHold * 256 + tid) * 8; k < K; k += 2048) {
+  for (int k = kHeld + tid * 8; k < K; k += 8 * LANES) {
     float g[8];
     load8<DT>(x, base + k, g);
 #pragma unroll
@@ -76,17 +101,20 @@ w8a8_quantize_kernel(const void* __restrict__ x, int64_t stride, int K, int8_t* 
   mag = lanes_max<64>(mag);
   if ((tid & 63) == 0) part[tid >> 6] = mag;
   __syncthreads();
-  mag = max(max(part[0], part[1]), max(part[2], part[3]));
+#pragma unroll
+  for (int i = 0; i < LANES / 64; ++i) mag = max(mag, part[i]);
   float s = scale_of(mag);
   if (s == 0.0f) s = 1.0f;
   const Codes8 q(s);
   int8_t* out = codes + row * (int64_t)K;
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) {
-    const int k = (i * 256 + tid) * 8;
-    if (k < K) *(u32x2_t*)(out + k) = codes8(f[i], q);
+  for (int i = 0; i < HOLD; ++i) {
+    const int k = (i * LANES + tid) * 8;
+    float f[8];
+    held(i, f);
+    if (k < K) *(u32x2_t*)(out + k) = codes8(f, q);
   }
-  for (int k = (kHold * 256 + tid) * 8; k < K; k += 2048) {
+  for (int k = kHeld + tid * 8; k < K; k += 8 * LANES) {
     float g[8];
     load8<DT>(x, base + k, g);
     *(u32x2_t*)(out + k) = codes8(g, q);
@@ -94,15 +122,22 @@ w8a8_quantize_kernel(const void* __restrict__ x, int64_t stride, int K, int8_t* 
   if (tid == 0) scales[row] = s;
 }
 
+template <int DT>
+void launch_quantize_dt(const void* x, int64_t M, int64_t K, int64_t stride, int8_t* codes,
+                        float* scales, hipStream_t st) {
+  if (M < kFewRows)
+    hipLaunchKernelGGL((w8a8_quantize_kernel<DT, 1024>), dim3((unsigned)M), dim3(1024), 0, st, x,
+                       stride, (int)K, codes, scales);
+  else
+    hipLaunchKernelGGL((w8a8_quantize_kernel<DT, 256>), dim3((unsigned)M), dim3(256), 0, st, x,
+                       stride, (int)K, codes, scales);
+}
+
 hipError_t launch_quantize(const void* x, int64_t M, int64_t K, int64_t stride, int dtype,
                            int8_t* codes, float* scales, hipStream_t st) {
-  const dim3 g((unsigned)M), b(256);
-  if (dtype == W4A16_F16)
-    hipLaunchKernelGGL(w8a8_quantize_kernel<DT_F16>, g, b, 0, st, x, stride, (int)K, codes, scales);
-  else if (dtype == W4A16_BF16)
-    hipLaunchKernelGGL(w8a8_quantize_kernel<DT_BF16>, g, b, 0, st, x, stride, (int)K, codes, scales);
-  else
-    hipLaunchKernelGGL(w8a8_quantize_kernel<2>, g, b, 0, st, x, stride, (int)K, codes, scales);
+  (dtype == W4A16_F16    ? launch_quantize_dt<DT_F16>
+   : dtype == W4A16_BF16 ? launch_quantize_dt<DT_BF16>
+                         : launch_quantize_dt<2>)(x, M, K, stride, codes, scales, st);
   return hipGetLastError();
 }
 
@@ -509,18 +544,20 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   }
 }
 
-// Few tokens: the call is the stream of w.  One workgroup of 8 waves per 16 NT
-// channels and all (at most 16 MB) tokens, on v_mfma_i32_16x16x64_i8; the waves
-// take the steps of 64 codes in turn, straight from memory into registers
-// (lane l: 16 codes of row l & 15), kAhead steps of a wave under way, and their
-// sums are joined in LDS.
+// Few tokens and channels: the call is the stream of w, spread over all CUs.
+// One workgroup of 8 waves per 16 NT channels and all (at most 16 MB) tokens, on
+// v_mfma_i32_16x16x64_i8; the waves take the steps of 128 codes (whole lines) in
+// turn, straight from memory into registers (lane l: 16 codes of row l & 15),
+// AHEAD steps of a wave under way, and their sums are joined in LDS.  MI355X: 16
+// x 4096 x 11008 in 12.5 us, of which 4 do not depend on K (launch, first
+// rows, join); the rest is w at 5.4 TB/s.
 //
 // FUSED: the tokens come in 16 bits, every workgroup quantizes them for itself
 // into LDS while its first rows of w are on their way; each of 512 lanes holds
 // 8 values of up to kRows rows of 4096 (a longer row counts as several).
-constexpr int kAhead = 4, kRows = 4;
+constexpr int kRows = 4;
 
-template <int DT, int MB, int NT, bool FUSED>
+template <int DT, int MB, int NT, bool FUSED, int AHEAD>
 __global__ void __launch_bounds__(512)
 w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __restrict__ sx,
                    const int8_t* __restrict__ wq, const float* __restrict__ sw,
@@ -534,19 +571,24 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int col0 = (int)blockIdx.x * 16 * NT;
-  const int KT = (K + 63) >> 6;
+  const int KT = (K + 127) >> 7;
   const rsrc_t rw = make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(16 * NT, N - col0) * (uint32_t)K);
   const uint32_t lane_off = (uint32_t)r * (uint32_t)K + 16u * g;
-  auto load_w = [&](int s, i32x4_t (&w)[NT]) {
-    const bool in = 64 * s + 16 * g < K;
+  auto load_w = [&](int s, i32x4_t (&w)[2][NT]) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-      w[i] = __builtin_bit_cast(
-          i32x4_t, bld128(rw, in ? lane_off + (uint32_t)(16 * i) * (uint32_t)K : kOutOfRange, s * 64));
-  };
-  i32x4_t w[kAhead][NT];
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) load_w(wave + 8 * u, w[u]);
+      for (int e = 0; e < 2; ++e)
+        w[e][i] = __builtin_bit_cast(
+            i32x4_t, bld128(rw,
+                            128 * s + 64 * e + 16 * g < K
+                                ? lane_off + (uint32_t)(16 * i) * (uint32_t)K + 64 * e
+                                : kOutOfRange,
+                            s * 128));
+  };
+  i32x4_t w[AHEAD][2][NT];
+#pragma unroll
+  for (int u = 0; u < AHEAD; ++u) load_w(wave + 8 * u, w[u]);
 
   rsrc_t rx;
   const int pitch = K + 16;  // FUSED: bytes of a row of codes in LDS
@@ -590,22 +632,24 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
     if (tid < 16 * MB) scales[tid] = tid < M ? sx[tid] : 0.0f;
   }
   // tokens past the last repeat it (their results are not written)
-  auto load_x = [&](int s, i32x4_t (&v)[MB]) {
+  auto load_x = [&](int s, i32x4_t (&v)[2][MB]) {
 #pragma unroll
-    for (int j = 0; j < MB; ++j) {
-      const int m = min(16 * j + r, M - 1);
-      if constexpr (FUSED)
-        v[j] = *(const i32x4_t*)(lds + m * pitch + min(64 * s + 16 * g, K - 16));
-      else
-        v[j] = __builtin_bit_cast(
-            i32x4_t, bld128(rx, 64 * s + 16 * g < K ? (uint32_t)m * (uint32_t)K + 16u * g : kOutOfRange,
-                            s * 64));
-    }
+    for (int j = 0; j < MB; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int m = min(16 * j + r, M - 1), k = 128 * s + 64 * e + 16 * g;
+        if constexpr (FUSED)
+          v[e][j] = *(const i32x4_t*)(lds + m * pitch + min(k, K - 16));
+        else
+          v[e][j] = __builtin_bit_cast(
+              i32x4_t, bld128(rx, k < K ? (uint32_t)m * (uint32_t)K + 64 * e + 16u * g : kOutOfRange,
+                              s * 128));
+      }
   };
-  i32x4_t xv[kAhead][MB];
+  i32x4_t xv[AHEAD][2][MB];
   if constexpr (!FUSED) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load_x(wave + 8 * u, xv[u]);
+    for (int u = 0; u < AHEAD; ++u) load_x(wave + 8 * u, xv[u]);
   }
 
   i32x4_t acc[NT][MB];
@@ -613,17 +657,20 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
-  for (int s0 = wave; s0 < KT; s0 += 8 * kAhead) {
+  for (int s0 = wave; s0 < KT; s0 += 8 * AHEAD) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < AHEAD; ++u) {
       if constexpr (FUSED) load_x(s0 + 8 * u, xv[u]);
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int j = 0; j < MB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][i], xv[u][j], acc[i][j], 0, 0, 0);
-      load_w(s0 + 8 * (u + kAhead), w[u]);
-      if constexpr (!FUSED) load_x(s0 + 8 * (u + kAhead), xv[u]);
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < MB; ++j)
+            acc[i][j] =
+                __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][e][i], xv[u][e][j], acc[i][j], 0, 0, 0);
+      load_w(s0 + 8 * (u + AHEAD), w[u]);
+      if constexpr (!FUSED) load_x(s0 + 8 * (u + AHEAD), xv[u]);
     }
   }
 
@@ -652,7 +699,8 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
 }
 
 // --------------------------------------------------------------- dispatch ---
-typedef Tile<2, 2, 2, 2, 4> T128;
+typedef Tile<2, 1, 2, 4, 4> T128;  // 128 x 128, 8 waves, alone on its CU
+typedef Tile<1, 1, 2, 2, 4> T64;   // 64 x 64, 4 waves, two on a CU
 
 // The operands of a call: 16-bit rows (with a stride) or codes with scales.
 struct Args {
@@ -676,41 +724,58 @@ void launch_tile(const Args& a, hipStream_t st) {
 
 template <int DT, int MB, int NT, bool FUSED>
 void launch_stream(const Args& a, hipStream_t st) {
-  launch_timed(w8a8_stream_kernel<DT, MB, NT, FUSED>, dim3((unsigned)ceil_div(a.N, 16 * NT)),
+  // rows of w under way per wave: where there is work before they are used,
+  // 4 steps in all (1 x 4096 x 4096: 9.1 us with one step, 8.0 with four);
+  // otherwise one, whose few registers leave room for a second workgroup
+  // (16 x 4096 x 11008: 12.5 us, 13.4 with four; 8 x 5120 x 16384: 28, 30.2)
+  constexpr int AHEAD = FUSED ? 4 / NT : 1;
+  launch_timed(w8a8_stream_kernel<DT, MB, NT, FUSED, AHEAD>, dim3((unsigned)ceil_div(a.N, 16 * NT)),
                dim3(512), 0, st, a.x, a.x_stride, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K);
-}
-
-// Channels per workgroup of the stream kernel: 64 where that leaves two
-// workgroups for each of 256 CUs, else 32, else 16.
-int stream_nt(int64_t N) { return N >= 512 * 64 ? 4 : N >= 512 * 32 ? 2 : 1; }
-
-template <int DT, int MB, bool FUSED>
-void launch_stream_nt(const Args& a, hipStream_t st) {
-  const int nt = stream_nt(a.N);
-  if (nt == 4 && MB <= 2) launch_stream<DT, MB, MB <= 2 ? 4 : 2, FUSED>(a, st);
-  else if (nt >= 2) launch_stream<DT, MB, 2, FUSED>(a, st);
-  else launch_stream<DT, MB, 1, FUSED>(a, st);
 }
 
 // Whether w8a8_linear quantizes inside the product.
 bool fused(int64_t M, int64_t K) { return M * ceil_div(K, 4096) <= kRows; }
 
 template <int DT>
+void launch_wide(const Args& a, hipStream_t st) {
+  const int mb = (int)ceil_div(a.M, 256), nb = (int)ceil_div(a.N, 256);
+  const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
+  launch_timed(w8a8_wide_kernel<DT>, dim3((unsigned)std::min(256, per_xcd * 8)), dim3(256), 0, st,
+               (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb, per_xcd);
+}
+
+// The kernel of a call.  A kernel's time per step of 128 codes was measured on
+// MI355X as 0.3 us for 64 x 64 tiles while there is at most one per CU, and in
+// proportion to their number beyond (two share a CU); 0.6 us per round of 256
+// tiles of 128 x 128; 1.6 us per round of 256 of 256 x 256.  The rule takes the
+// least sum.  Both sides of its borders (M x N x K, us):
+//   64 / 128:   128 x 16384 x 5120 32.8 / 34.6, 512 x 1016 x 11008 26.3 / 38.1,
+//               333 x 7168 x 5120 31.3 / 23.2, 512 x 5120 x 5120 30.8 / 23.6
+//   128 / 256:  1024 x 5120 x 5120 46.0 / 55.4, 2048 x 4096 x 4096 46.9 / 50.4,
+//               512 x 16384 x 5120 68.2 / 68.6, 2048 x 5120 x 5120 73.6 / 64.1,
+//               1024 x 16384 x 5120 121.5 / 84.0
+// and for few tokens by few channels, where 64 x 64 tiles are too few to ask
+// memory for w at its rate, the stream kernel (stream / 64 x 64):
+//   16 x 4096 x 11008 12.5 / 24.6, 16 x 8192 x 4096 11.2 / 11.8,
+//   16 x 12288 x 4096 14.7 / 12.0, 32 x 4096 x 4096 8.8 / 11.6,
+//   32 x 8192 x 4096 14.5 / 11.7, 64 x 4096 x 4096 12.5 / 12.0
+template <int DT>
 hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
-  if (a.M > 512) {
-    const int mb = (int)ceil_div(a.M, 256), nb = (int)ceil_div(a.N, 256);
-    const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
-    launch_timed(w8a8_wide_kernel<DT>, dim3((unsigned)std::min(256, per_xcd * 8)), dim3(256), 0, st,
-                 (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb,
-                 per_xcd);
-  } else if (a.M > 64) {
+  const int64_t t64 = ceil_div(a.M, 64) * ceil_div(a.N, 64);
+  const int64_t t128 = ceil_div(a.M, 128) * ceil_div(a.N, 128);
+  const int64_t t256 = ceil_div(a.M, 256) * ceil_div(a.N, 256);
+  const int64_t c64 = 3 * std::max<int64_t>(t64, 256), c128 = 6 * 256 * ceil_div(t128, 256),
+                c256 = 16 * 256 * ceil_div(t256, 256);
+  if (a.M <= 64 && ceil_div(a.M, 16) * a.N < 12288) {
+    if (a.M > 32) launch_stream<DT, 4, 1, false>(a, st);
+    else if (a.M > 16) launch_stream<DT, 2, 1, false>(a, st);
+    else launch_stream<DT, 1, 1, false>(a, st);
+  } else if (c64 <= c128 && c64 <= c256) {
+    launch_tile<DT, T64>(a, st);
+  } else if (c128 <= c256) {
     launch_tile<DT, T128>(a, st);
-  } else if (a.M > 32) {
-    launch_stream_nt<DT, 4, false>(a, st);
-  } else if (a.M > 16) {
-    launch_stream_nt<DT, 2, false>(a, st);
   } else {
-    launch_stream_nt<DT, 1, false>(a, st);
+    launch_wide<DT>(a, st);
   }
   return hipGetLastError();
 }
@@ -722,13 +787,21 @@ hipError_t launch_gemm(const int8_t* xq, const float* sx, const int8_t* wq, cons
   return (dtype == DT_F16 ? launch_gemm_dt<DT_F16> : launch_gemm_dt<DT_BF16>)(a, st);
 }
 
+// Channels per workgroup: 64 where that leaves two workgroups for each of 256
+// CUs, else 32, else 16 (each reads and quantizes the tokens for itself).
+template <int DT>
+void launch_fused_dt(const Args& a, hipStream_t st) {
+  if (a.N >= 512 * 64) launch_stream<DT, 1, 4, true>(a, st);
+  else if (a.N >= 512 * 32) launch_stream<DT, 1, 2, true>(a, st);
+  else launch_stream<DT, 1, 1, true>(a, st);
+}
+
 hipError_t launch_fused(const void* x, int64_t x_stride, const int8_t* wq, const float* sw,
                         const void* bias, void* out, int64_t M, int64_t N, int64_t K, int dtype,
                         hipStream_t st) {
   const Args a = {x, x_stride, nullptr, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M,
                   (int)N, (int)K};
-  if (dtype == DT_F16) launch_stream_nt<DT_F16, 1, true>(a, st);
-  else launch_stream_nt<DT_BF16, 1, true>(a, st);
+  (dtype == DT_F16 ? launch_fused_dt<DT_F16> : launch_fused_dt<DT_BF16>)(a, st);
   return hipGetLastError();
 }
 

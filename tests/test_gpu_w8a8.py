@@ -89,6 +89,32 @@ def test_product(M, N, K, dtype):
     assert torch.equal(y, plain)
 
 
+@pytest.mark.parametrize("M,N,K", [(16, 12296, 160), (48, 4104, 272), (320, 8200, 144), (700, 4872, 400),
+                                   (1100, 16392, 112), (2100, 5128, 208)])
+def test_a_result_does_not_depend_on_the_kernel(M, N, K):
+    """Each call against the same rows and channels in small calls, bit for bit (copies: scales are read 16 bytes at a time)."""
+    say("w8a8 whole and parts", M, N, K)
+    xq, wq = _codes(M, M, K).to(DEV), _codes(N + 1, N, K).to(DEV)
+    xs, ws = (_normal(2, M).abs() * 1e-3 + 1e-4).to(DEV), (_normal(3, N).abs() * 1e-2).to(DEV)
+    bias = _normal(4, N).bfloat16().to(DEV)
+    y = w4.w8a8_gemm(xq, xs, wq, ws, bias)
+    for rows in (slice(0, 9), slice(M // 2, M // 2 + 40), slice(M - 8, M)):
+        for cols in (slice(0, 64), slice(N - 2056, N)):
+            part = w4.w8a8_gemm(xq[rows].clone(), xs[rows].clone(), wq[cols].clone(),
+                                ws[cols].clone(), bias[cols].clone())
+            assert torch.equal(y[rows, cols], part), (rows, cols)
+
+
+def test_quantize_many_rows_as_each_alone():
+    for M, K in ((512, 2064), (513, 2064), (1200, 16400)):
+        say("quantize many rows", M, K)
+        x = (_normal(M, M, K) * torch.logspace(-3, 3, M)[:, None]).bfloat16().to(DEV)
+        c, s = w4.w8a8_quantize(x)
+        for m in (0, 1, M // 2, M - 1):
+            cm, sm = w4.w8a8_quantize(x[m:m + 1])
+            assert torch.equal(c[m:m + 1], cm) and torch.equal(s[m:m + 1], sm)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 131072), (70, 48, 131072), (300, 264, 131072)])
 def test_the_longest_sum_is_exact(M, N, K):
     say("w8a8 longest", M, N, K)
