@@ -4,7 +4,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <cstring>
 #include <initializer_list>
 
 #include "../../include/w4a16.h"
@@ -46,16 +45,7 @@ inline int validate_dtype(int32_t dtype) {
   return (dtype == W4A16_F16 || dtype == W4A16_BF16) ? W4A16_OK : W4A16_ERR_INVALID_ARG;
 }
 
-// Copies a plan's text to a caller's buffer, truncated to fit and terminated;
-// its full length.
-inline int64_t copy_names(const char* s, char* names_host, int64_t names_bytes) {
-  const int64_t len = (int64_t)std::strlen(s);
-  if (names_bytes > 0) {
-    const int64_t n = len < names_bytes - 1 ? len : names_bytes - 1;
-    std::memcpy(names_host, s, (size_t)n);
-    names_host[n] = 0;
-  }
-  return len;
-}
+// Bytes rounded up to the parts a workspace is divided in.
+inline int64_t pad256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace w4a16

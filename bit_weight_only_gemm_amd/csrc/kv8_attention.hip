@@ -433,18 +433,20 @@ __device__ __forceinline__ int swizzle(int row) {
 //    all banks.
 //
 // WHOLE: pages of 64 tokens and more, a unit lies in one page.
-template <int DT, int D, int W, bool WHOLE>
-__global__ void __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(1, 2)))
+template <int D>
+constexpr int kPromptWaves = D / 16;
+
+template <int DT, int D, bool WHOLE>
+__global__ void __launch_bounds__(64 * kPromptWaves<D>) __attribute__((amdgpu_waves_per_eu(1, 2)))
 kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float scale, int causal,
                   uint16_t* __restrict__ out, int64_t out_stride, float* __restrict__ lse,
                   Parts parts, int row_tiles, int splits, int units) {
   // in iteration u the keys of u + 1 and the values of u are read, and both of
   // u + 2 written
-  constexpr int NBK = 2, NBV = 3;
+  constexpr int NBK = 2, NBV = 3, W = kPromptWaves<D>;
   constexpr int KS = D / 16, DN = D / 32, ROWS = 32 * W;
   constexpr int BUF = kUnit * D * 2;                // fp16 keys (or values) of a unit
-  constexpr int CH = kUnit * D / 16 / (64 * W);     // 16-byte pieces of each per lane
-  static_assert(CH >= 1, "a piece for every lane");
+  static_assert(kUnit * D == 64 * W * 16, "a 16-byte piece of each for every lane");
   // two waves to a SIMD: 256 registers each, the queries wait in LDS
   constexpr bool Q_LDS = W == 8;
   __shared__ __attribute__((aligned(16))) uint8_t lds[(NBK + NBV) * BUF + (Q_LDS ? ROWS * D * 2 : 0)];
@@ -502,51 +504,40 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     }
   }
 
-  // ---- staging: piece i of this lane is 16 bytes at 16 (64 W i + tid) of the
-  // unit's [4 subtiles][16 D]
+  // ---- staging: this lane's piece is 16 bytes at 16 tid of the unit's [4
+  // subtiles][16 D]
   const int64_t page_bytes = (int64_t)D << c.lgT;
   const int T = 1 << c.lgT;
   const int32_t* table = c.table + (int64_t)b * c.width;
-  u32x4_t kw[CH], vw[CH];
-  // table entries of this lane's pieces of a unit, and of its 16 tokens of
+  u32x4_t kw, vw;
+  // table entries of this lane's piece of a unit, and of its 16 tokens of
   // each 32 (WHOLE: one for all), units past the last repeating it; they are
   // brought into range where they are used, a unit later
-  constexpr int NP = WHOLE ? 1 : CH, NSC = WHOLE ? 1 : 2;
-  int of_piece[NP], of_scale[NSC];
+  constexpr int NSC = WHOLE ? 1 : 2;
+  const int sub = tid / D, in_sub = tid % D * 16;
+  int of_piece, of_scale[NSC];
   auto entry = [&](int u, int token) {
     return table[min((min(u, nu - 1) * kUnit + token) >> c.lgT, c.width - 1)];
   };
   auto turn_pages = [&](int u_pieces, int u_scales) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-      of_piece[i] = entry(u_pieces, WHOLE ? 0 : 16 * ((64 * W * i + tid) / D));
+    of_piece = entry(u_pieces, WHOLE ? 0 : 16 * sub);
 #pragma unroll
     for (int a = 0; a < NSC; ++a) of_scale[a] = entry(u_scales, WHOLE ? 0 : 32 * a + 16 * h);
   };
   // (the empty statements hold a loaded value's first use where it stands)
   auto fetch = [&](int u) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) asm volatile("" : "+v"(of_piece[i]));
+    asm volatile("" : "+v"(of_piece));
+    const int t = min(u, nu - 1) * kUnit;
+    int64_t from;
     if constexpr (WHOLE) {
-      const int page = clamp_int(__builtin_amdgcn_readfirstlane(of_piece[0]), 0, c.pages - 1);
-      const int64_t from = ((int64_t)page * c.Hkv + hk) * page_bytes +
-                           (int64_t)((min(u, nu - 1) * kUnit) & (T - 1)) * D;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        kw[i] = *(const u32x4_t*)(c.k + from + (64 * W * i + tid) * 16);
-        vw[i] = *(const u32x4_t*)(c.v + from + (64 * W * i + tid) * 16);
-      }
+      const int page = clamp_int(__builtin_amdgcn_readfirstlane(of_piece), 0, c.pages - 1);
+      from = ((int64_t)page * c.Hkv + hk) * page_bytes + (int64_t)(t & (T - 1)) * D + tid * 16;
     } else {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int byte = (64 * W * i + tid) * 16, sub = byte / (16 * D);
-        const int t = min(u, nu - 1) * kUnit + 16 * sub;
-        const int64_t from = ((int64_t)clamp_int(of_piece[i], 0, c.pages - 1) * c.Hkv + hk) * page_bytes +
-                             (t & (T - 1)) * D + byte % (16 * D);
-        kw[i] = *(const u32x4_t*)(c.k + from);
-        vw[i] = *(const u32x4_t*)(c.v + from);
-      }
+      from = ((int64_t)clamp_int(of_piece, 0, c.pages - 1) * c.Hkv + hk) * page_bytes +
+             ((t + 16 * sub) & (T - 1)) * D + in_sub;
     }
+    kw = *(const u32x4_t*)(c.k + from);
+    vw = *(const u32x4_t*)(c.v + from);
   };
   float ks_next[NSC], vs_next[NSC];
   auto fetch_scales = [&]() {
@@ -558,27 +549,19 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       vs_next[a] = c.vs[at_s];
     }
   };
-  // part j of CH * 4: half a piece of keys or values to its buffer.  A key
-  // (token 16 sub + tk of the unit) is row 32 (sub >> 1) + the bits of its place
-  // in 32 tokens in the order 0, 1, subtile's parity, 2, 3.  Where the pieces
-  // lie whole 32s of tokens apart, one address of each kind serves them all.
-  auto key_place = [&](int i) {
-    const int byte = (64 * W * i + tid) * 16, sub = byte / (16 * D);
-    const int tk = byte % (16 * D) / D, ch = byte % D / 16;
-    const int row = 32 * (sub >> 1) + (tk & 3) + 4 * (sub & 1) + 8 * (tk >> 2);
-    return row * D * 2 + (((2 * ch) ^ swizzle<D>(row)) << 4);
-  };
-  constexpr bool EVEN = 64 * W * 16 % (32 * D) == 0;
-  int k_place = key_place(0), v_place = (tid / D * 2 * D + tid % D) * 16;
+  // part j of 4: half a piece of keys or values to its buffer.  A key (token 16
+  // sub + tk of the unit) is row 32 (sub >> 1) + the bits of its place in 32
+  // tokens in the order 0, 1, subtile's parity, 2, 3.
+  const int tk = in_sub / D, k_row = 32 * (sub >> 1) + (tk & 3) + 4 * (sub & 1) + 8 * (tk >> 2);
+  int k_place = k_row * D * 2 + (((in_sub % D / 8) ^ swizzle<D>(k_row)) << 4);
+  int v_place = (sub * 2 * D + tid % D) * 16;
   auto stage = [&](int j, int kbuf, int vbuf) {
-    const int i = j >> 2, e = j & 1;
-    if (j & 2) {  // a channel's tokens 16 sub + 8 e ..
-      *(half8_t*)(lds + (NBK + vbuf) * BUF + v_place + (64 * W / D * i * 2 + e) * D * 16) =
-          codes_f16(vw[i][2 * e], vw[i][2 * e + 1]);
-    } else {      // a token's channels 16 ch + 8 e ..
-      const int at_k = EVEN ? k_place + 64 * W * 32 * i : key_place(i);
-      *(half8_t*)(lds + kbuf * BUF + (at_k ^ e << 4)) = codes_f16(kw[i][2 * e], kw[i][2 * e + 1]);
-    }
+    const int e = j & 1;
+    if (j & 2)  // a channel's tokens 16 sub + 8 e ..
+      *(half8_t*)(lds + (NBK + vbuf) * BUF + v_place + e * D * 16) =
+          codes_f16(vw[2 * e], vw[2 * e + 1]);
+    else        // a token's channels 16 ch + 8 e ..
+      *(half8_t*)(lds + kbuf * BUF + (k_place ^ e << 4)) = codes_f16(kw[2 * e], kw[2 * e + 1]);
   };
 
   float m = -1e30f, l = 0.0f, ref = 0.0f;
@@ -684,7 +667,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     }
     // ---- the second product, and between its steps the staging of the unit
     // after the next
-    constexpr int N2 = 4 * DN, PARTS = 4 * CH;
+    constexpr int N2 = 4 * DN, PARTS = 4;
 #pragma unroll
     for (int k = 0; k < 3; ++k) fr[k] = value(vbuf, k);
 #pragma unroll
@@ -712,11 +695,11 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     fetch_scales();
     turn_pages(u0 + 1, u0 + 1);
 #pragma unroll
-    for (int j = 0; j < 4 * CH; ++j) stage(j, 0, 0);
+    for (int j = 0; j < 4; ++j) stage(j, 0, 0);
     fetch(u0 + 1);
     turn_pages(u0 + 2, u0 + 1);
 #pragma unroll
-    for (int j = 0; j < 4 * CH; ++j) stage(j, 1, 1);
+    for (int j = 0; j < 4; ++j) stage(j, 1, 1);
     fetch(u0 + 2);
     turn_pages(u0 + 3, u0 + 1);
     __syncthreads();
@@ -834,7 +817,7 @@ struct Plan {
 Plan plan_attention(int64_t B, int64_t max_new, int64_t max_len, int H, int Hkv, int D) {
   Plan p;
   const int64_t rows = max_new * (H / Hkv);
-  p.waves = rows <= 128 ? 0 : D == 64 ? 4 : 8;
+  p.waves = rows <= 128 ? 0 : D == 64 ? kPromptWaves<64> : kPromptWaves<128>;
   p.rows = p.waves ? 32 * p.waves : 16;
   p.row_tiles = (int)ceil_div(rows, p.rows);
   const int64_t nu = std::max<int64_t>(1, ceil_div(max_len, kUnit));
@@ -845,8 +828,6 @@ Plan plan_attention(int64_t B, int64_t max_new, int64_t max_len, int H, int Hkv,
   p.splits = (int)std::min(ceil_div(nu, p.units), want);
   return p;
 }
-
-int64_t pad256(int64_t b) { return ceil_div(b, 256) * 256; }
 
 // The workspace begins with the decode kernel's counters, at the same place
 // in every call: they are zero between calls, whatever the calls' sizes.
@@ -870,11 +851,10 @@ hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t 
                  p.splits, p.units);
   };
   const int64_t grid = 8 * ceil_div(groups, 8) * p.row_tiles;
-  constexpr int WAVES = D == 64 ? 4 : 8;
   const bool whole = (1 << c.lgT) >= kUnit;
   if (p.waves == 0) go(kv8_decode_kernel<DT, D>, grid, 256);
-  else if (whole) go(kv8_prompt_kernel<DT, D, WAVES, true>, grid, 64 * WAVES);
-  else go(kv8_prompt_kernel<DT, D, WAVES, false>, grid, 64 * WAVES);
+  else if (whole) go(kv8_prompt_kernel<DT, D, true>, grid, 64 * kPromptWaves<D>);
+  else go(kv8_prompt_kernel<DT, D, false>, grid, 64 * kPromptWaves<D>);
   if (p.waves && p.splits > 1)
     hipLaunchKernelGGL((kv8_join_kernel<DT, D>),
                        dim3((unsigned)ceil_div((int64_t)c.B * max_new * c.H, 4)), dim3(256), 0,

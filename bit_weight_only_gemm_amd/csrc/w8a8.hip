@@ -815,8 +815,6 @@ int validate_shape(int64_t M, int64_t N, int64_t K) {
   return W4A16_OK;
 }
 
-int64_t pad256(int64_t b) { return ceil_div(b, 256) * 256; }
-
 // w8a8_linear's codes and scales
 int64_t linear_bytes(int64_t M, int64_t K) { return pad256(M * K) + pad256(M * 4); }
 
