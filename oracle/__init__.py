@@ -25,6 +25,8 @@ intb   -- the same at 3, 4 or 8 bits (bit-stream packing of 32-code runs).
 nf4    -- NF4 codebook (closed form), block quantizer, double quant, dequant.
 gemm   -- fp64 reference product and the relative-error score.
 repack -- reference implementation of the repacked tile layout and its inverse.
+w8a8   -- 8-bit integer product with token and channel scales, its error bound.
+kv8    -- paged 8-bit key/value cache: rotation, page order, attention, bounds.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against closed forms, brute force, exact rational arithmetic or independent
@@ -32,4 +34,4 @@ library routines.  Bit-compatibility with third-party checkpoints or libraries
 is "parity unpinned": the pages give no byte layout for them.
 """
 
-from . import fp, int4, intb, nf4, gemm, repack  # noqa: F401
+from . import fp, int4, intb, kv8, nf4, gemm, repack, w8a8  # noqa: F401
