@@ -137,6 +137,14 @@ __device__ __forceinline__ float four_rows_max(float x) {
 // tokens 16 g + 4 a + i (g = l >> 4) of the unit in register i of product a,
 // which is the operand layout of the second product: neither keys, values
 // nor probabilities pass through LDS.
+//
+// The cache's bytes bound it where there are many: 64 ragged sequences of up to
+// 8192 tokens, 40 / 8 heads of 128, 136 us, 5.1 TB/s of codes (MI355X; a plain
+// read gets 5.7); 3 of up to 131001, 119 us.  Few tokens are a chain of waits
+// (length, table, keys, values, join): one sequence of 777, 32 heads, 10.3 us.
+// With 16 rows to a wave and not more, three waves share a SIMD and cover each
+// other's waits: 32 or 48 rows a wave read the codes less often, and took 27 us
+// against 21 for 24 sequences of 4001, 40 rows of 64 channels a kv head.
 template <int DT, int D>
 __global__ void __launch_bounds__(256)
 kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float scale, int causal,
@@ -431,6 +439,13 @@ __device__ __forceinline__ int swizzle(int row) {
 //    Keys: rows of 2 D bytes, their 16-byte chunks permuted by row; values:
 //    [16 tokens][8 of them][channel] pieces of 16 bytes.  Reads and writes meet
 //    all banks.
+//
+// The matrix and the vector unit share the time: a unit of 64 tokens costs a
+// wave 2 D / 16 products of 32 cycles, and some 600 vector operations for its
+// probabilities.  MI355X, 4 sequences of 2048 new over 8192, D = 128: 40 / 8 heads
+// 1391 us (865 TFLOP/s), 32 / 32 heads 918 TFLOP/s, matrix units busy 46 %;
+// D = 64: 678 TFLOP/s.  Ragged chunks of up to 2048 over up to 8192 take 1065 us,
+// 2161 in the decode kernel's form.
 //
 // WHOLE: pages of 64 tokens and more, a unit lies in one page.
 template <int D>
