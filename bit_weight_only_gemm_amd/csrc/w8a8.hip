@@ -351,14 +351,19 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 //    before run.  Steps go on across tiles: a tile's first rows and operands
 //    arrive during the last step and the results of the tile before.
 //  * The results pass through LDS of their own into whole 128-byte pieces of
-//    y's rows; the tile's scales and bias wait there since its first step.
+//    y's rows; the tile's scales and bias wait there since its first step, in
+//    one of two places by the tile's parity: no barrier stands between a tile's
+//    results and the first step of the next, which writes the other place, and
+//    before a wave writes this one again it passes a barrier that every wave
+//    reaches only after these results.
 //
 // The matrix units bound it, at the clock the card holds under them: 8192 x
 // 55296 x 5120 in 1850 us, 2.5 PFLOP/s, the units busy 69 % of the cycles (2.57
 // with every load from L2, 2.82 without loads; with one tile per workgroup and
 // loads straight to LDS it took 2324 us).
 constexpr int kWideStage = 512 * 128, kWideTurn = 2 * kWideStage, kWideScales = kWideTurn + 4 * 4096;
-constexpr int kWideLds = kWideScales + 256 * 12;  // x's scales, w's, the bias as fp32
+// x's scales, w's, the bias as fp32; of this tile and of the one before
+constexpr int kWideLds = kWideScales + 2 * 256 * 12;
 
 template <int DT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
@@ -466,7 +471,8 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   read(0, 0, fw[0], fx[0]);
   int slot = 0;
   float sx_v = 0.0f, sw_v = 0.0f, bias_v = 0.0f;
-  float* scales = (float*)(lds + kWideScales);
+  int turn = 0;  // the tile's place of scales
+  auto scales_at = [&](int i) { return (float*)(lds + kWideScales + turn * 256 * 12) + i; };
   auto step = [&](auto anew) {
     read(slot, 1, fw[1], fx[1]);
 #pragma unroll
@@ -485,9 +491,9 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     order(std::integral_constant<int, 4>{});
     loaded();
     if (decltype(anew)::value) {
-      scales[tid] = sx_v;
-      scales[256 + tid] = sw_v;
-      scales[512 + tid] = bias_v;
+      *scales_at(tid) = sx_v;
+      *scales_at(256 + tid) = sw_v;
+      *scales_at(512 + tid) = bias_v;
     }
     // the next step is whole in LDS, and nobody reads this one any more
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -522,11 +528,11 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     const int r = at_lane & 31, h = at_lane >> 5;
 #pragma unroll
     for (int i0 = 0; i0 < 4; i0 += 2) {
-      const float* sn = scales + 256 + wn * 128 + i0 * 32 + 4 * h;
+      const float* sn = scales_at(256 + wn * 128 + i0 * 32 + 4 * h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int mrow = row0 + (wm * 4 + j) * 32;
-        const float s = scales[(wm * 4 + j) * 32 + r];
+        const float s = *scales_at((wm * 4 + j) * 32 + r);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -552,6 +558,7 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
         __builtin_amdgcn_wave_barrier();
       }
     }
+    turn ^= 1;
   }
 }
 
