@@ -726,11 +726,10 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   }
   int vb = 0;
   auto turn = [&](auto edge, float16_t (&now)[2], float16_t (&next)[2], int u, int parity) {
-    if (u > u0) {
-      // the keys of u + 1 and the values of u are whole in LDS, and nobody
-      // reads any more what this iteration overwrites
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    }
+    // the keys of u + 1 and the values of u are whole in LDS, and nobody reads
+    // any more what this iteration overwrites: in the first one the keys of u0,
+    // of which every wave has formed its scores just above
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     const int vb2 = vb == 0 ? 2 : vb - 1;  // (vb + 2) % 3
     unit(edge, now, next, u, parity ^ 1, vb, parity, vb2);
     vb = vb == 2 ? 0 : vb + 1;
