@@ -29,7 +29,8 @@ def _empty(shape, dtype, device, stream=None):
 
 def _rows(t, dtypes, name, K=None):
     """Checks a matrix of rows [..., K] whose last dimension is contiguous and
-    whose rows are evenly spaced; (rows, K, row stride in elements)."""
+    whose rows are evenly spaced and do not overlap; (rows, K, row stride in
+    elements)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if t.dtype not in dtypes:
@@ -48,7 +49,10 @@ def _rows(t, dtypes, name, K=None):
     if one != 1 and shape[-1] > 1:
         raise ValueError("%s must be contiguous within a row" % name)
     M = t.shape[0]
-    return M, shape[-1], max(step, shape[-1]) if M > 1 else shape[-1]
+    if M > 1 and step < shape[-1]:      # expanded or overlapping rows
+        raise ValueError("%s must have rows at least %d elements apart, got %d"
+                         % (name, shape[-1], step))
+    return M, shape[-1], step if M > 1 else shape[-1]
 
 
 def _at(t):

@@ -64,3 +64,15 @@ def test_linear_of_many_tiles():
     for n in range(0, N, 2048):
         b = slice(n, n + 2048)
         assert torch.equal(y[:, b], w4.w8a8_linear(x, wq[b].clone(), ws[b].clone(), bias[b].clone())), n
+
+
+def test_expanded_and_overlapping_rows_are_refused():
+    wq, ws = w4.w8a8_quantize(torch.ones(16, 64, device=DEV))
+    row = torch.ones(1, 64, dtype=torch.float16, device=DEV)
+    over = torch.ones(160, dtype=torch.float16, device=DEV).as_strided((5, 64), (16, 1))
+    for x in (row.expand(5, 64), row[0].expand(2, 3, 64), over):
+        with pytest.raises(ValueError, match="elements apart"):
+            w4.w8a8_quantize(x)
+        with pytest.raises(ValueError, match="elements apart"):
+            w4.w8a8_linear(x, wq, ws)
+    assert torch.equal(w4.w8a8_linear(row.expand(1, 64), wq, ws), w4.w8a8_linear(row, wq, ws))
