@@ -48,4 +48,9 @@ inline int validate_dtype(int32_t dtype) {
 // Bytes rounded up to the parts a workspace is divided in.
 inline int64_t pad256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
+// HIP takes grids of less than 2^32 work-items.
+inline bool too_large(int64_t workgroups, int64_t threads) {
+  return workgroups > (((int64_t)1 << 32) - 1) / threads;
+}
+
 }  // namespace w4a16

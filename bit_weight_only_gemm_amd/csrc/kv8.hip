@@ -171,6 +171,27 @@ __device__ void turn_queries(const Kv8& c, const Rope& rope, const uint16_t* q, 
   }
 }
 
+// Room of the pages that sequences b' < b touch: n new tokens lie in at most
+// n / T + 2 pages, so sequence b's pages have the places [at(b), at(b + 1)) of
+// tokens / T + 2 B in all.
+__device__ __forceinline__ int pages_before(const Kv8& c, int b) {
+  return (clamp_int(c.cu[b], 0, c.tokens) >> c.lgT) + 2 * b;
+}
+
+// The sequence that has place s, by the whole wave: 64 sequences at a look.
+__device__ __forceinline__ int sequence_at(const Kv8& c, int s) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = c.B;
+  while (n > 1) {
+    const int step = (n + 63) >> 6, i = min(lane * step, n - 1);
+    const uint64_t before = __ballot(lane * step < n && pages_before(c, lo + i) <= s);
+    const int skip = max(__popcll(before) - 1, 0) * step;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
 // Several new tokens.  One workgroup per (sequence, touched page, kv head, keys
 // or values), the only one to touch those bytes and that scale.  The new rows
 // are read once and kept, rotated, in registers; the page's scale is the larger
@@ -286,7 +307,7 @@ template <int DT, int D, int PASSES>
 __global__ void __launch_bounds__(256)
 kv8_append_kernel(Kv8 c, Rope rope, const uint16_t* q, int64_t q_stride,
                   uint16_t* q_out, int64_t qo_stride, const uint16_t* __restrict__ k,
-                  int64_t k_stride, const uint16_t* __restrict__ v, int64_t v_stride, int chunks,
+                  int64_t k_stride, const uint16_t* __restrict__ v, int64_t v_stride,
                   int64_t blocks) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[PASSES * 4096];
   __shared__ uint32_t part[4];
@@ -297,8 +318,9 @@ kv8_append_kernel(Kv8 c, Rope rope, const uint16_t* q, int64_t q_stride,
   }
   const bool values = id & 1;
   const int64_t j = id >> 1;
-  const int head = (int)(j % c.Hkv), chunk = (int)(j / c.Hkv % chunks);
-  const int b = (int)(j / c.Hkv / chunks);
+  const int head = (int)(j % c.Hkv), place = (int)(j / c.Hkv);
+  const int b = __builtin_amdgcn_readfirstlane(sequence_at(c, place));
+  const int chunk = max(place - pages_before(c, b), 0);
   append_page<DT, D, PASSES>(c, rope, values ? v : k, values ? v_stride : k_stride, values, b,
                              chunk, head, lds, part);
 }
@@ -455,15 +477,18 @@ kv8_dequant_kernel(const uint8_t* __restrict__ k, const uint8_t* __restrict__ v,
 template <int DT, int D, int PASSES>
 void launch_append_p(const Kv8& c, const Rope& rope, const void* q, int64_t q_stride, void* q_out,
                      int64_t qo_stride, const void* k, int64_t k_stride, const void* v,
-                     int64_t v_stride, int64_t max_new, hipStream_t st) {
-  // a run of max_new tokens touches at most this many pages
-  const int64_t T = (int64_t)1 << c.lgT, chunks = (max_new + T - 2) / T + 1;
-  const int64_t blocks = chunks * c.B * c.Hkv * 2;
-  const int64_t qblocks = q ? c.tokens : 0;
+                     int64_t v_stride, int64_t blocks, int64_t qblocks, hipStream_t st) {
   hipLaunchKernelGGL((kv8_append_kernel<DT, D, PASSES>), dim3((unsigned)(blocks + qblocks)),
                      dim3(256), 0, st, c, rope, (const uint16_t*)q, q_stride, (uint16_t*)q_out,
                      qo_stride, (const uint16_t*)k, k_stride, (const uint16_t*)v, v_stride,
-                     (int)chunks, blocks);
+                     blocks);
+}
+
+// Workgroups of an append (those that turn queries aside).  The places of pages
+// go by all new tokens, not by the largest number in a sequence: 256 sequences
+// with a few long ones among them have some B places and not B times the longest.
+int64_t append_blocks(int64_t tokens, int64_t B, int64_t T, int Hkv, int D, int64_t max_new) {
+  return max_new == 1 ? ceil_div(B * Hkv * 2, 256 / (D / 16)) : (tokens / T + 2 * B) * Hkv * 2;
 }
 
 template <int DT>
@@ -472,11 +497,11 @@ hipError_t launch_append(const Kv8& c, const Rope& rope, int D, const void* q, i
                          const void* v, int64_t v_stride, int64_t max_new, hipStream_t st) {
 #define W4A16_APPEND(DD, P)                                                                    \
   launch_append_p<DT, DD, P>(c, rope, q, q_stride, q_out, qo_stride, k, k_stride, v, v_stride, \
-                             max_new, st)
+                             blocks, qblocks, st)
   const int T = 1 << c.lgT;
+  const int64_t blocks = append_blocks(c.tokens, c.B, T, c.Hkv, D, max_new);
+  const int64_t qblocks = q ? c.tokens : 0;
   if (max_new == 1) {
-    const int64_t blocks = ceil_div((int64_t)c.B * c.Hkv * 2, 256 / (D / 16));
-    const int64_t qblocks = q ? c.tokens : 0;
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks + qblocks)), dim3(256), 0, st, c, rope,
                          (const uint16_t*)q, q_stride, (uint16_t*)q_out, qo_stride,
@@ -533,8 +558,8 @@ int kv8_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_strid
     for (const void* p : {q, (const void*)q_out, (const void*)cu_seqlens, (const void*)cos,
                           (const void*)sin})
       if (!aligned16(p)) return W4A16_ERR_MISALIGNED;
-    const int64_t T = page_size, chunks = (max_new + T - 2) / T + 1;
-    if (chunks * B * Hkv * 2 + tokens > ((int64_t)1 << 31) - 1) return W4A16_ERR_UNSUPPORTED;
+    if (too_large(append_blocks(tokens, B, page_size, Hkv, D, max_new) + (q ? tokens : 0), 256))
+      return W4A16_ERR_UNSUPPORTED;
     clear_pending_error();
     const Kv8 c = {k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens,
                    (int)num_pages, (int)max_pages, (int)B, (int)tokens, H, Hkv,
@@ -561,7 +586,7 @@ int kv8_dequant(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_s
     const int64_t heads = n * Hkv, per = (int64_t)page_size * D;
     const int64_t k_blocks = ceil_div(heads * (per / 16), 256);
     const int64_t blocks = k_blocks + ceil_div(heads * (per / 128), 256);
-    if (blocks > ((int64_t)1 << 31) - 1) return W4A16_ERR_UNSUPPORTED;
+    if (too_large(blocks, 256)) return W4A16_ERR_UNSUPPORTED;
     const dim3 g((unsigned)blocks), b(256);
     const hipStream_t st = (hipStream_t)stream;
     auto go = [&](auto kernel) {

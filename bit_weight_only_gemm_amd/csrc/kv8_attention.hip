@@ -919,8 +919,8 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
     const Plan p = plan_attention(B, max_new, max_len, H, Hkv, D);
     const int64_t need = part_bytes(p, tokens, H, D);
     if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
-    if (8 * ceil_div(B * Hkv * p.splits, 8) * p.row_tiles > ((int64_t)1 << 31) - 1 ||
-        B * max_new * H > ((int64_t)1 << 32))
+    // (the join's grid is smaller: it runs where there are less than 512 row tiles)
+    if (too_large(8 * ceil_div(B * Hkv * p.splits, 8) * p.row_tiles, p.waves ? 64 * p.waves : 256))
       return W4A16_ERR_UNSUPPORTED;
     clear_pending_error();
     const Kv8 c = {const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(v_cache),

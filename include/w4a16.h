@@ -559,7 +559,9 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
  * multiple of 8, at least heads * D), so slices of a fused projection can be
  * passed as they are.
  * Limits (W4A16_ERR_UNSUPPORTED): tokens <= 2^24, B <= 2^20, H <= 1024,
- * max_pages * T <= 2^30, num_pages <= 2^30, grids below 2^31 workgroups.
+ * max_pages * T <= 2^30, num_pages <= 2^30, and grids of 2^32 work-items,
+ * which are reached by tokens + 2 Hkv (tokens / T + 2 B) of 2^24 in an append
+ * and by B * H * max_new of about 2^31 in an attention.
  * tokens, B or max_new of 0 launches nothing.
  */
 
