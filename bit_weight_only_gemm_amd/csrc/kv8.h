@@ -27,14 +27,16 @@ struct Kv8 {
   const int32_t* table;  // [B, width]
   const int32_t* lens;   // [B] tokens of each sequence, the new ones included
   const int32_t* cu;     // [B + 1] first new token of each sequence, or null: one each
-  int pages, width, B, tokens, H, Hkv, lgT;
+  int pages, width, B, tokens, max_new, H, Hkv, lgT;
 };
 
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
-// Sequence b: its first new token and their count, and its length.
+// Sequence b: its first new token, how many of them are processed (at most
+// max_new), the first one's position (below 0 where there are more new tokens
+// than the sequence has), and its length.
 struct Kv8Seq {
-  int tok, n, len;
+  int tok, n, first, len;
 };
 __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8& c, int b) {
   Kv8Seq s;
@@ -46,6 +48,8 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8& c, int b) {
     s.n = 1;
   }
   s.len = (int)min((int64_t)max(c.lens[b], 0), (int64_t)c.width << c.lgT);
+  s.first = s.len - s.n;
+  s.n = min(s.n, c.max_new);
   return s;
 }
 __device__ __forceinline__ int kv8_page(const Kv8& c, int b, int index) {

@@ -143,8 +143,9 @@ __device__ void turn_queries(const Kv8& c, const Rope& rope, const uint16_t* q, 
     b = lo;
   }
   const Kv8Seq s = kv8_seq(c, b);
+  if (tok - s.tok >= s.n) return;
   const Place p = place_of(rope, threadIdx.x % L, true);
-  const Angles g = angles_of(rope, p, s.len - s.n + tok - s.tok);
+  const Angles g = angles_of(rope, p, s.first + tok - s.tok);
   const uint16_t* src = q + (int64_t)tok * q_stride;
   uint16_t* dst = out + (int64_t)tok * o_stride;
   constexpr int AT_ONCE = 4;
@@ -209,11 +210,11 @@ __device__ void append_page(const Kv8& c, const Rope& rope, const uint16_t* x, i
                             bool values, int b, int chunk, int head, uint8_t* lds,
                             uint32_t* part) {
   const Kv8Seq q = kv8_seq(c, b);
-  const int T = 1 << c.lgT, start = max(q.len - q.n, 0);
+  const int T = 1 << c.lgT, start = max(q.first, 0), end = q.first + q.n;
   const int p = (start >> c.lgT) + chunk;
-  if (q.len == 0 || (p << c.lgT) >= q.len || q.n == 0) return;
-  const int r0 = max(start - (p << c.lgT), 0), r1 = min(q.len - (p << c.lgT), T);
-  const int tok0 = q.tok + q.n - (q.len - (p << c.lgT));  // new token of the page's row 0
+  if (q.n == 0 || (p << c.lgT) >= end) return;
+  const int r0 = max(start - (p << c.lgT), 0), r1 = min(end - (p << c.lgT), T);
+  const int tok0 = q.tok + (p << c.lgT) - q.first;  // new token of the page's row 0
   const int page = kv8_page(c, b, p);
   const int64_t slot = (int64_t)page * c.Hkv + head;
   uint8_t* dst = (values ? c.v : c.k) + slot * ((int64_t)T * D);
@@ -350,9 +351,9 @@ kv8_append_token_kernel(Kv8 c, Rope rope, const uint16_t* q, int64_t q_stride,
   const int64_t bq = (row >> 1) / c.Hkv;
   const int b = (int)min(bq, (int64_t)c.B - 1);
   const Kv8Seq sq = kv8_seq(c, b);
-  const bool on = bq < c.B && sq.len > 0 && sq.n > 0;
-  const int T = 1 << c.lgT, pos = max(sq.len - 1, 0), r0 = pos & (T - 1);
-  const int tok = sq.tok + max(sq.n - 1, 0);
+  const bool on = bq < c.B && sq.first >= 0 && sq.n > 0;
+  const int T = 1 << c.lgT, pos = max(sq.first, 0), r0 = pos & (T - 1);
+  const int tok = sq.tok;
   const Place at = place_of(rope, threadIdx.x % L, !values);
   const uint16_t* x = (values ? v + (int64_t)tok * v_stride : k + (int64_t)tok * k_stride) + head * D;
   u32x4_t w0 = {0, 0, 0, 0}, w1 = {0, 0, 0, 0};
@@ -562,7 +563,7 @@ int kv8_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_strid
       return W4A16_ERR_UNSUPPORTED;
     clear_pending_error();
     const Kv8 c = {k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens,
-                   (int)num_pages, (int)max_pages, (int)B, (int)tokens, H, Hkv,
+                   (int)num_pages, (int)max_pages, (int)B, (int)tokens, (int)max_new, H, Hkv,
                    log2_page(page_size)};
     const Rope rope = {cos, sin, (int)rope_rows, rope_dim, interleaved};
     return hip_status((dtype == DT_F16 ? launch_append<DT_F16> : launch_append<DT_BF16>)(

@@ -86,7 +86,7 @@ __device__ __forceinline__ float queries_f16(const u32x4_t (&w)[N], half8_t (&ou
 // Query rows of a (sequence, kv head): row i is token i / G, head i % G.  A
 // row tile is `rows` of them; it sees keys up to the largest limit of its rows.
 __device__ __forceinline__ int row_limit(const Kv8Seq& s, int causal, int j) {
-  return causal ? clamp_int(s.len - s.n + j + 1, 0, s.len) : s.len;
+  return causal ? clamp_int(s.first + j + 1, 0, s.len) : s.len;
 }
 __device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, int rows, int G) {
   return row_limit(s, causal, min((rt * rows + rows - 1) / G, s.n - 1));
@@ -925,8 +925,8 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
     clear_pending_error();
     const Kv8 c = {const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(v_cache),
                    const_cast<float*>(k_scale), const_cast<float*>(v_scale), page_table, seq_lens,
-                   cu_seqlens, (int)num_pages, (int)max_pages, (int)B, (int)tokens, H, Hkv,
-                   log2_page(page_size)};
+                   cu_seqlens, (int)num_pages, (int)max_pages, (int)B, (int)tokens, (int)max_new, H,
+                   Hkv, log2_page(page_size)};
     auto* f = D == 64 ? (dtype == DT_F16 ? launch_attention<DT_F16, 64>
                                          : launch_attention<DT_BF16, 64>)
                       : (dtype == DT_F16 ? launch_attention<DT_F16, 128>

@@ -550,11 +550,12 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
  * at positions seq_lens[b] - n .. seq_lens[b] - 1, n their count (0 is
  * legal); cu_seqlens NULL: one new token for each sequence, in order (tokens
  * == B).  max_new is an upper bound of n (<= tokens; 1 with cu_seqlens NULL);
- * rows past it in a sequence are not processed.  Tables, lengths and offsets
+ * rows past it in a sequence, and rows of no sequence, are not processed:
+ * neither stored nor written to q_out or out.  Tables, lengths and offsets
  * stay on the device: entries out of range are brought into range, so they
  * give unspecified values but no access outside the arrays; table entries
  * past a sequence's last page are not used.  A token at a negative position
- * (n > seq_lens[b]) is not stored and sees nothing.
+ * (n > seq_lens[b]) is not stored and, when causal, sees nothing.
  * Rows of q, k, v and out are [heads][D] with a row stride in elements (a
  * multiple of 8, at least heads * D), so slices of a fused projection can be
  * passed as they are.
