@@ -28,8 +28,10 @@ constexpr int kUnit = 64;  // tokens a wave takes at a time
 // fp16's range, and exact to 2^-11 down to 2^-25 of the largest (2^-36 of it
 // absolutely below that); the sum takes w (u / vs).  vs / u is held to kLeast and
 // up, where every w is 0 in fp16, so that a page of zeros divides nothing by 0.
+// u is at least kRef, the least that has a reciprocal; pages of subnormal scales
+// below it lose part of the lift instead.
 // Sums of both products carry the factor 2^kLift, which their quotient drops.
-constexpr float kLift = 11.0f, kLag = 3.0f, kLeast = 0x1p-45f;
+constexpr float kLift = 11.0f, kLag = 3.0f, kLeast = 0x1p-45f, kRef = 0x1p-126f;
 
 // log(sum exp) of a row, natural, from its maximum and sum.
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -280,8 +282,9 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     mx = four_rows_max(mx * f);
     float back = 1.0f;
     if (vs_top > 2.0f * ref) {
-      back = ref / vs_top;
-      ref = vs_top;
+      const float to = fmaxf(vs_top, kRef);
+      back = ref * __builtin_amdgcn_rcpf(to);
+      ref = to;
     }
     if (__any(mx > m + kLag) || back != 1.0f) {
       const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
@@ -633,8 +636,9 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     mx = both_halves_max(mx);
     float back = 1.0f;
     if (vs_top > 2.0f * ref) {
-      back = ref / vs_top;
-      ref = vs_top;
+      const float to = fmaxf(vs_top, kRef);
+      back = ref * __builtin_amdgcn_rcpf(to);
+      ref = to;
     }
     if (__any(mx > m + kLag) || back != 1.0f) {
       const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
@@ -763,7 +767,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     }
     return;
   }
-  const float inv = l == 0.0f ? 0.0f : ref / l;  // a row that sees nothing is 0
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing is 0
   uint16_t* dst = out + (int64_t)tok * out_stride + head * D;
 #pragma unroll
   for (int i = 0; i < DN; ++i)
@@ -771,7 +775,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     for (int j = 0; j < 4; ++j) {
       uint32_t y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = round16<DT>(o[i][4 * j + e] * inv);
+      for (int e = 0; e < 4; ++e) y[e] = round16<DT>(o[i][4 * j + e] * inv * ref);
       *(u32x2_t*)(dst + 32 * i + 8 * j + 4 * h) = u32x2_t{y[0] | y[1] << 16, y[2] | y[3] << 16};
     }
   if (lse && h == 0)
