@@ -31,6 +31,15 @@ constexpr int kUnit = 64;  // tokens a wave takes at a time
 // u is at least kRef, the least that has a reciprocal; pages of subnormal scales
 // below it lose part of the lift instead.
 // Sums of both products carry the factor 2^kLift, which their quotient drops.
+//
+// m is the rounded product of a sum and its factor, and one fma forms a score's
+// distance from it: exact but for m's own rounding, 2^-24 |m|, which all of a
+// row's probabilities share.  From |m| = 2^24 on that is a factor fp16 cannot
+// hold, and kLift is lost beside m; so where m of a row passes kFar, scores are
+// rounded as m was and m is subtracted first.  (kFar is low so that the factor,
+// 2^-14 there, does not tell keys seen before the change from those after.)  A
+// row's m before its first key is kNone, the least of fp32.
+constexpr float kFar = 0x1p10f, kNone = -0x1.fffffep127f;
 constexpr float kLift = 11.0f, kLag = 3.0f, kLeast = 0x1p-45f, kRef = 0x1p-126f;
 
 // log(sum exp) of a row, natural, from its maximum and sum.
@@ -199,7 +208,8 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     for (int i = 0; i < 2 * DC; ++i) qf[i >> 1][i & 1] = f[i];
   }
 
-  float m = -1e30f, l = 0.0f, ref = 0.0f;
+  float m = kNone, l = 0.0f, ref = 0.0f;
+  bool far = false;  // m of some row of the wave has passed kFar
   float4_t o[DN];
 #pragma unroll
   for (int i = 0; i < DN; ++i) o[i] = float4_t{};
@@ -295,10 +305,20 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       for (int i = 0; i < DN; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] *= both;
+      far = far || __any(fabsf(m) > kFar && m != kNone);
+    }
+    float off = m;
+    if (__builtin_expect(far, false)) {
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[a][i] = s[a][i] * f - m;
+      f = 1.0f;
+      off = 0.0f;
     }
     const float q_v = v_scale * (ref > 0.0f ? __builtin_amdgcn_rcpf(ref) : 0.0f);
     const float ratio = q_v < kLeast ? kLeast : q_v;
-    const float shift = __builtin_amdgcn_logf(ratio) + kLift - m;
+    const float shift = __builtin_amdgcn_logf(ratio) + kLift - off;
     half8_t pf[2];
     float sum = 0.0f;
 #pragma unroll
@@ -582,7 +602,8 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       *(half8_t*)(lds + kbuf * BUF + (k_place ^ e << 4)) = codes_f16(kw[2 * e], kw[2 * e + 1]);
   };
 
-  float m = -1e30f, l = 0.0f, ref = 0.0f;
+  float m = kNone, l = 0.0f, ref = 0.0f;
+  bool far = false;  // m of some row of the wave has passed kFar
   float16_t o[DN], even[2], odd[2];  // scores of the units 0, 2, .. and 1, 3, ..
 #pragma unroll
   for (int i = 0; i < DN; ++i) o[i] = float16_t{};
@@ -649,6 +670,18 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       for (int i = 0; i < DN; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] *= both;
+      far = far || __any(fabsf(m) > kFar && m != kNone);
+    }
+    float off = m;
+    if (__builtin_expect(far, false)) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[a][i] = s[a][i] * f[WHOLE ? 0 : a] - m;
+      }
+#pragma unroll
+      for (int a = 0; a < NSC; ++a) f[a] = 1.0f;
+      off = 0.0f;
     }
     __builtin_amdgcn_sched_barrier(0);
     // ---- the next unit's scores, one product at a time, and between them this
@@ -660,7 +693,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     for (int a = 0; a < NSC; ++a) {
       const float q_v = vs[a] * over;
       ratio[a] = q_v < kLeast ? kLeast : q_v;
-      shift[a] = __builtin_amdgcn_logf(ratio[a]) + kLift - m;
+      shift[a] = __builtin_amdgcn_logf(ratio[a]) + kLift - off;
       sum[a] = 0.0f;
     }
     constexpr int N1 = 2 * KS, PER = 32 / N1;

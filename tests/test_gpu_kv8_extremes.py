@@ -75,3 +75,53 @@ def test_tiny_values_through_the_append():
     w4.kv8_append(cache, k, v, table, lens, cu)
     _check(cache, q, table.cpu().numpy(), [200], [0, 200], "bf16", 0.125)
     _check(cache, q[-1:], table.cpu().numpy(), [200], [0, 1], "bf16", 0.125)
+
+
+def _onehot_scores(q, cache, r, power):
+    """Queries of one channel each and keys whose scores are small integers
+    times 2^power: exact in fp32, far apart where they differ, often equal."""
+    D = q.shape[2]
+    channel = torch.from_numpy(r.randint(0, D, q.shape[:2])).to(DEV)
+    q.zero_()
+    half = min(power // 2, 14 if q.dtype == torch.float16 else 120)
+    q.scatter_(2, channel[..., None], 2.0 ** half)
+    codes = r.randint(-5, 6, cache["k"].shape)
+    cache["k"].copy_(torch.from_numpy((codes + 128).astype(np.uint8)))
+    scales = 2.0 ** r.randint(0, 3, cache["k_scale"].shape)
+    cache["k_scale"].copy_(torch.from_numpy(scales.astype(np.float32)))
+    return 2.0 ** (power - half)
+
+
+@pytest.mark.parametrize("news,D,T", FORMS)
+@pytest.mark.parametrize("power,dtype", [(18, "f16"), (24, "bf16"), (27, "f16"), (31, "bf16"), (38, "f16"),
+                                         (60, "bf16"), (99, "bf16"), (120, "bf16")])
+def test_scores_of_any_magnitude(power, dtype, news, D, T):
+    """The rows' largest scores take it all, in equal parts, whatever the
+    magnitude and sign: probabilities are exact, the output is off by its sums'
+    roundings (64 tokens and the joins) and its own."""
+    say("scores of 2 **", power, dtype, news, D, T)
+    cache, q, table, lens, cu, r = _case(power, news, D, T, dtype)
+    scale = _onehot_scores(q, cache, r, power)
+    dev = lambda x: torch.from_numpy(np.asarray(x, np.int32)).to(DEV)  # noqa: E731
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = w4.kv8_attention(q, cache, dev(table), dev(lens), dev(cu), max_new=max(news), scale=scale, lse=lse)
+    ks, vs = (cache[n].cpu().numpy().astype(np.float64)[:, :, None, None] for n in ("k_scale", "v_scale"))
+    k, v = kv8.rows_k(cache["k"].cpu().numpy()) * ks, kv8.rows_v(cache["v"].cpu().numpy()) * vs
+    want, mass, lw, _ = kv8.attention(q.double().cpu().numpy(), k, v, table, lens, cu, T, scale, True)
+    bound, _ = kv8.attention_bounds(want, mass, np.zeros(lw.shape), max(lens), D, dtype)
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert np.all(err <= bound), (np.max(err / bound), np.argwhere(~(err <= bound))[:4])
+    l = lse.double().cpu().numpy()
+    assert np.all(np.abs(l - lw) <= 2.0 ** -18 + 2.0 ** -22 * np.abs(lw))
+
+
+@pytest.mark.parametrize("news,D,T", FORMS)
+@pytest.mark.parametrize("scale", [1e6, 1e7, 1e8, 1e10, 1e30, -1e34])
+def test_large_scores_stay_among_the_values(scale, news, D, T):
+    say("scale", scale, news, D, T)
+    cache, q, table, lens, cu, r = _case(3, news, D, T, "bf16")
+    dev = lambda x: torch.from_numpy(np.asarray(x, np.int32)).to(DEV)  # noqa: E731
+    out = w4.kv8_attention(q, cache, dev(table), dev(lens), dev(cu), max_new=max(news), scale=scale)
+    most = 127 * cache["v_scale"].max() * (1 + 2.0 ** -8)
+    assert torch.isfinite(out).all() and torch.all(out.abs() <= most)
+    assert torch.all(out.abs().amax(2) > 0)
