@@ -42,9 +42,15 @@ constexpr int kUnit = 64;  // tokens a wave takes at a time
 constexpr float kFar = 0x1p10f, kNone = -0x1.fffffep127f;
 constexpr float kLift = 11.0f, kLag = 3.0f, kLeast = 0x1p-45f, kRef = 0x1p-126f;
 
-// log(sum exp) of a row, natural, from its maximum and sum.
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.0f ? -INFINITY : (m + __log2f(l) - kLift) * kLn2;
+// Results that are still to be joined are o u and l, both times 2^-kShrink: an o
+// of up to 2^38 (codes, weights and tokens) would leave fp32 at values of 1e28,
+// and l, 2^8 and more where it counts, keeps the products of bf16's least values
+// above fp32's.
+constexpr float kShrink = 20.0f, kPart = 0x1p-20f;
+
+// log(sum exp) of a row, natural, from its maximum and its sum times 2^-shrunk.
+__device__ __forceinline__ float lse_of(float m, float l, float shrunk) {
+  return l == 0.0f ? -INFINITY : (m + (__log2f(l) + (shrunk - kLift))) * kLn2;
 }
 
 typedef float float16_t __attribute__((ext_vector_type(16)));
@@ -356,10 +362,10 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
 
   // ---- join the waves: lane holds channels 16 i + 4 g + j of row col
 #pragma unroll
-  for (int i = 0; i < DN; ++i) *(float4_t*)&joined[wave][col][16 * i + 4 * g] = o[i] * ref;
+  for (int i = 0; i < DN; ++i) *(float4_t*)&joined[wave][col][16 * i + 4 * g] = o[i] * kPart * ref;
   if (g == 0) {
     stat[wave][0][col] = m;
-    stat[wave][1][col] = l;
+    stat[wave][1][col] = l * kPart;
   }
   __syncthreads();
   // 16 lanes per row
@@ -438,7 +444,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     *(uint32_t*)(out + tk * out_stride + hd * D + channel(j)) =
         (uint32_t)round16<DT>(r[j] * inv) | (uint32_t)round16<DT>(r[j + 1] * inv) << 16;
   if (lse && part == 0)
-    lse[tk * c.H + hd] = lse_of(mm, ll);
+    lse[tk * c.H + hd] = lse_of(mm, ll, kShrink);
 }
 
 // Position of a key row's 16-byte chunks in LDS (rows of 2 D bytes): 16 lanes
@@ -790,13 +796,12 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     for (int i = 0; i < DN; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4_t v = {o[i][4 * j] * ref, o[i][4 * j + 1] * ref, o[i][4 * j + 2] * ref,
-                            o[i][4 * j + 3] * ref};
-        *(float4_t*)(parts.o + at_p * D + 32 * i + 8 * j + 4 * h) = v;
+        const float4_t v = {o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+        *(float4_t*)(parts.o + at_p * D + 32 * i + 8 * j + 4 * h) = v * kPart * ref;
       }
     if (h == 0) {
       parts.ml[at_p * 2] = m;
-      parts.ml[at_p * 2 + 1] = l;
+      parts.ml[at_p * 2 + 1] = l * kPart;
     }
     return;
   }
@@ -812,7 +817,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       *(u32x2_t*)(dst + 32 * i + 8 * j + 4 * h) = u32x2_t{y[0] | y[1] << 16, y[2] | y[3] << 16};
     }
   if (lse && h == 0)
-    lse[(int64_t)tok * c.H + head] = lse_of(m, l);
+    lse[(int64_t)tok * c.H + head] = lse_of(m, l, 0.0f);
 }
 
 // Joins the prompt kernel's splits of a row, in their order: one wave per
@@ -848,7 +853,7 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
 #pragma unroll
   for (int e = 0; e < E; ++e)
     out[(seq.tok + j) * out_stride + hd * D + lane * E + e] = round16<DT>(r[e] * inv);
-  if (lse && lane == 0) lse[row] = lse_of(m, l);
+  if (lse && lane == 0) lse[row] = lse_of(m, l, kShrink);
 }
 
 // waves: of the prompt kernel's workgroups (32 rows each); 0: the decode kernel.

@@ -125,3 +125,17 @@ def test_large_scores_stay_among_the_values(scale, news, D, T):
     most = 127 * cache["v_scale"].max() * (1 + 2.0 ** -8)
     assert torch.isfinite(out).all() and torch.all(out.abs() <= most)
     assert torch.all(out.abs().amax(2) > 0)
+
+
+@pytest.mark.parametrize("news,D,T,lens", [(n, D, T, (150, 210)) for n, D, T in FORMS]
+                         + [([1, 1], 64, 16, (3000, 2100)), ([1, 1], 128, 64, (3000, 2100)),
+                            ([70, 40], 128, 32, (3000, 2100))])
+@pytest.mark.parametrize("low,high", [(24, 27), (30, 32), (33, 34), (-3, 35)])
+def test_values_near_the_largest(low, high, news, D, T, lens):
+    """Values of up to 1e37, in parts that are joined: over waves, and over
+    workgroups where the sequences are long."""
+    say("large values", low, high, news, D, T, lens)
+    cache, q, table, lens, cu, r = _case(4, news, D, T, "bf16", lens)
+    cache["v_scale"].copy_(torch.from_numpy(10.0 ** r.uniform(low, high, cache["v_scale"].shape)).float())
+    out = _check(cache, q, table, lens, cu, "bf16", D ** -0.5)
+    assert torch.isfinite(out).all()
