@@ -109,6 +109,11 @@ __device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, i
   return row_limit(s, causal, min((rt * rows + rows - 1) / G, s.n - 1));
 }
 
+// Units of a split: this sequence's in equal shares, none below the planned.
+__device__ __forceinline__ int split_units(int nu, int splits, int units) {
+  return max(units, (nu + splits - 1) / splits);
+}
+
 // Partial results of a split: O [row][split][D], then (m, l) [row][split],
 // row = token * H + head; and one counter for each (sequence, kv head, row
 // tile) of the decode kernel, 0 between calls.
@@ -186,8 +191,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   if (rt * 16 >= seq.n * G) return;
   const int top = tile_limit(seq, causal, rt, 16, G);
   const int nu = (top + kUnit - 1) / kUnit;
-  // this sequence's units in equal shares, none below `units`
-  const int share = max(units, (nu + splits - 1) / splits);
+  const int share = split_units(nu, splits, units);
   const int u0 = split * share, u1 = min(u0 + share, nu);
   if (split > 0 && u0 >= nu) return;
 
@@ -511,7 +515,8 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   if (rt * ROWS >= seq.n * G) return;
   const int top = tile_limit(seq, causal, rt, ROWS, G);
   const int nu = (top + kUnit - 1) / kUnit;
-  const int u0 = split * units, u1 = min(u0 + units, nu);
+  const int share = split_units(nu, splits, units);
+  const int u0 = split * share, u1 = min(u0 + share, nu);
   if (split > 0 && u0 >= nu) return;
 
   const int row0 = rt * ROWS + wave * 32, ridx = row0 + col;
@@ -835,7 +840,8 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
   if (j >= seq.n) return;
   const int top = tile_limit(seq, causal, (j * G + hd % G) / rows, rows, G);
   const int nu = (top + kUnit - 1) / kUnit;
-  const int n = clamp_int((nu + units - 1) / units, 1, splits);
+  const int share = split_units(nu, splits, units);
+  const int n = max((nu + share - 1) / share, 1);
   const int64_t row = (int64_t)(seq.tok + j) * c.H + hd;
   float m = -INFINITY;
   for (int s = 0; s < n; ++s) m = fmaxf(m, parts.ml[(row * splits + s) * 2]);

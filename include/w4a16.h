@@ -622,8 +622,8 @@ int64_t kv8_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t max_new
  * as fp16 (bf16 rows after an exact power of two); one rounding to dtype.
  *   lse       fp32 [tokens][H] or NULL: log(sum exp(scale q . K)), natural.
  *   max_len   an upper bound of the seq_lens (<= max_pages * T), by which the
- *             split of the keys is planned; longer sequences are cut to
- *             the planned units.
+ *             split of the keys is planned (no more than that: longer
+ *             sequences are seen whole).
  *   workspace required where kv8_attention_workspace_bytes is not 0
  *             (W4A16_ERR_WORKSPACE when NULL or smaller).  Filled with zeros
  *             before its first use and used by kv8_attention alone: it holds
