@@ -86,8 +86,7 @@ __device__ __forceinline__ uint32_t mag16(const float (&f)[16]) {
   return m;
 }
 
-// 16 stored codes requantized to a scale `ratio` = old / new times as fine;
-// only the bytes of tokens in [0, keep) change when `tokens`, else all.
+// 16 stored codes requantized to a scale that is 1 / ratio (new / old) times theirs.
 __device__ __forceinline__ u32x4_t requantized(u32x4_t w, float ratio) {
   u32x4_t r = {0, 0, 0, 0};
 #pragma unroll

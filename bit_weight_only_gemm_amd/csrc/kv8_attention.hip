@@ -523,10 +523,8 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const bool rv = ridx < seq.n * G;
   const int tok = seq.tok + (rv ? ridx / G : 0), head = hk * G + (rv ? ridx % G : 0);
   const int lim = rv ? row_limit(seq, causal, ridx / G) : 0;
-  // keys that every row of this wave sees, and that any does
+  // keys that every row of this wave sees
   const int lim_all = row0 + 31 < seq.n * G ? row_limit(seq, causal, row0 / G) : 0;
-  const int lim_any =
-      row0 < seq.n * G ? row_limit(seq, causal, min(row0 + 31, seq.n * G - 1) / G) : 0;
 
   half8_t qf[Q_LDS ? 1 : KS];
   uint8_t* q_mine = lds + (NBK + NBV) * BUF + (wave * KS * 64 + lane) * 16;
@@ -862,9 +860,11 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
   if (lse && lane == 0) lse[row] = lse_of(m, l, kShrink);
 }
 
-// waves: of the prompt kernel's workgroups (32 rows each); 0: the decode kernel.
-constexpr int64_t kCounters = 16384;
+// A call is split into this many workgroups or more, so one that is split has
+// fewer row tiles, each of which has a counter.
+constexpr int64_t kWanted = 512, kCounters = kWanted;
 
+// waves: of the prompt kernel's workgroups (32 rows each); 0: the decode kernel.
 struct Plan {
   int waves, rows, row_tiles, splits, units;
 };
@@ -887,9 +887,8 @@ Plan plan_attention(int64_t B, int64_t max_new, int64_t max_len, int H, int Hkv,
   p.row_tiles = (int)ceil_div(rows, p.rows);
   const int64_t nu = std::max<int64_t>(1, ceil_div(max_len, kUnit));
   const int64_t groups = B * Hkv * p.row_tiles;
-  const int64_t want = std::max<int64_t>(1, ceil_div(512, groups));
+  const int64_t want = ceil_div(kWanted, groups);
   p.units = (int)(p.waves ? std::max<int64_t>(4, ceil_div(nu, want)) : 8);
-  if (groups > kCounters) p.units = (int)nu;
   p.splits = (int)std::min(ceil_div(nu, p.units), want);
   return p;
 }

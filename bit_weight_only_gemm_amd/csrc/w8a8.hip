@@ -7,7 +7,6 @@
 // The sum is exact in int32 (|c| <= 127 and K <= 2^17), so it does not depend
 // on any split of K.
 #include <algorithm>
-#include <cstdio>
 #include <type_traits>
 
 #include "abi.h"
@@ -869,8 +868,7 @@ int w8a8_gemm(const int8_t* xq, const float* x_scale, const int8_t* wq, const fl
     if (int s = validate_dtype(dtype)) return s;
     if (int s = check_ptrs({xq, x_scale, wq, w_scale, out})) return s;
     if (!aligned16(bias) || !aligned16(workspace)) return W4A16_ERR_MISALIGNED;
-    if (workspace && workspace_bytes < w8a8_workspace_bytes(M, N, K, 0))
-      return W4A16_ERR_WORKSPACE;
+    (void)workspace_bytes;  // none is needed
     clear_pending_error();
     return hip_status(launch_gemm(xq, x_scale, wq, w_scale, bias, out, M, N, K, dtype,
                                   (hipStream_t)stream));

@@ -92,7 +92,8 @@ def kv8_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, max_new=None,
     """Appends k, v [tokens, Hkv, D] to the cache, the keys rotated by their
     positions (cos, sin fp32 [positions, rope_dim / 2]), and returns the
     rotated queries q [tokens, H, D] (None without q).  max_new: an upper bound
-    of the new tokens of one sequence (all of them when not given)."""
+    of the new tokens of one sequence (all of them when not given; the kernel
+    for single tokens runs where it is 1); rows past it are not processed."""
     pages, Hkv, T, D, arrays = _cache(cache)
     tokens, _, k_stride = _heads(k, None, "k", None, Hkv, D)
     dtype = k.dtype
@@ -159,7 +160,12 @@ def kv8_attention(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
     """Attention of q [tokens, H, D] over the cached tokens of their sequences:
     [tokens, H, D] in q's dtype.  scale: 1 / sqrt(D) when not given; max_new,
     max_len: upper bounds of the new tokens and of the length of one sequence
-    (all tokens, the table's width); lse: fp32 [tokens, H], written if given."""
+    (all tokens, the table's width), by which the kernel and the split of the
+    keys are chosen: pass them where cu_seqlens is.  Rows past max_new are not
+    processed.  lse: fp32 [tokens, H], written if given.  workspace: one of
+    kv8_attention_workspace_bytes, kept for these calls alone and zero before
+    the first (one per stream is kept when not given): it holds counters, and
+    one that another operator has written in leaves results unwritten."""
     pages, Hkv, T, D, arrays = _cache(cache)
     tokens, H, q_stride = _heads(q, None, "q", None, None, D)
     dtype = q.dtype

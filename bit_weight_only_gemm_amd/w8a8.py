@@ -60,7 +60,7 @@ def _at(t):
 
 
 def w8a8_workspace_bytes(M, N, K, linear=True):
-    """Bytes that w8a8_linear (or, linear=False, w8a8_gemm) needs at this shape."""
+    """Bytes that w8a8_linear (or, linear=False, w8a8_gemm: 0) needs at this shape."""
     n = int(_lib.lib().w8a8_workspace_bytes(M, N, K, int(linear)))
     if n < 0:
         raise _lib.W4A16Error("w8a8_workspace_bytes: invalid shape M=%d N=%d K=%d" % (M, N, K))
@@ -109,7 +109,8 @@ def _space(workspace, need, device, stream, kept=None):
 def w8a8_gemm(xq, x_scale, wq, w_scale, bias=None, dtype=torch.bfloat16, out=None,
               workspace=None, use_workspace=True, stream=None):
     """y = (xq @ wq^T) * x_scale * w_scale + bias in ``dtype`` (fp16 or bf16)
-    for codes xq [..., K], wq [N, K] from w8a8_quantize."""
+    for codes xq [..., K], wq [N, K] from w8a8_quantize.  workspace and
+    use_workspace are taken as by the other products; no shape needs one."""
     if dtype not in _DT:
         raise TypeError("dtype must be float16 or bfloat16")
     N, K = _weights(wq, w_scale, bias, dtype)
@@ -119,12 +120,7 @@ def w8a8_gemm(xq, x_scale, wq, w_scale, bias=None, dtype=torch.bfloat16, out=Non
     M = xq.numel() // K
     _need(x_scale, torch.float32, "x_scale", M)
     out = _output(out, (*xq.shape[:-1], N), dtype, xq.device, stream)
-    nbytes = 0
-    if use_workspace:
-        need = max(0, int(_lib.lib().w8a8_workspace_bytes(M, N, K, 0)))
-        workspace, nbytes = _space(workspace, need, xq.device, stream)
-    else:
-        workspace = None
+    workspace, nbytes = _space(workspace if use_workspace else None, 0, xq.device, stream)
     _lib.check(_lib.lib().w8a8_gemm(_at(xq), _at(x_scale), _at(wq), _at(w_scale), _at(bias),
                                     _at(out), M, N, K, _DT[dtype], _at(workspace), nbytes,
                                     _stream(stream)), "w8a8_gemm")
@@ -133,7 +129,9 @@ def w8a8_gemm(xq, x_scale, wq, w_scale, bias=None, dtype=torch.bfloat16, out=Non
 
 def w8a8_linear(x, wq, w_scale, bias=None, out=None, workspace=None, stream=None):
     """y = x @ (wq * w_scale)^T + bias for x [..., K] fp16/bf16, quantized per
-    row on the way (w8a8_quantize and w8a8_gemm in one call)."""
+    row on the way (w8a8_quantize and w8a8_gemm in one call).  workspace: one of
+    w8a8_workspace_bytes (kept per stream when not given); it is written over,
+    so never kv8_attention's."""
     N, K = _weights(wq, w_scale, bias, x.dtype)
     M, _, stride = _rows(x, _DT, "x", K)
     dtype = x.dtype

@@ -515,7 +515,8 @@ int64_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t linear);
  * The product of quantized rows.
  *   xq int8 [M, K], x_scale fp32 [M]; wq int8 [N, K], w_scale fp32 [N];
  *   bias [N] in dtype or NULL; out [M, N] in dtype.
- *   workspace: optional, as for w4a16_gemm.
+ *   workspace: not used (w8a8_workspace_bytes is 0 at every shape); NULL or
+ *             16-byte aligned.
  * Async.  Bitwise reproducible.
  */
 int w8a8_gemm(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
@@ -619,7 +620,10 @@ int64_t kv8_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t max_new
  * (causal != 0), or all seq_lens[b] of them.  A query that sees nothing gives
  * 0 (and lse -inf).  Scores, the softmax's maximum and sum and the output
  * are held in fp32; probabilities enter the second product as fp16, queries
- * as fp16 (bf16 rows after an exact power of two); one rounding to dtype.
+ * as fp16 (bf16 rows after an exact power of two); one rounding to dtype.  A
+ * probability is off by 2^-11 of itself, and by up to 2^-36 of the row's largest
+ * times the ratio of the largest value scale seen to its page's: pages whose
+ * values are 2^-25 and less of other pages' are coarser.
  *   lse       fp32 [tokens][H] or NULL: log(sum exp(scale q . K)), natural.
  *   max_len   an upper bound of the seq_lens (<= max_pages * T), by which the
  *             split of the keys is planned (no more than that: longer
@@ -627,7 +631,9 @@ int64_t kv8_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t max_new
  *   workspace required where kv8_attention_workspace_bytes is not 0
  *             (W4A16_ERR_WORKSPACE when NULL or smaller).  Filled with zeros
  *             before its first use and used by kv8_attention alone: it holds
- *             counters that every call leaves at zero.
+ *             counters that every call leaves at zero.  With others in them (a
+ *             buffer that w8a8_linear has written its codes to) the rows whose
+ *             keys are split are not written.
  * Async.  Bitwise reproducible (splits are joined in order).
  */
 int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
