@@ -201,9 +201,9 @@ __device__ __forceinline__ int sequence_at(const Kv8& c, int s) {
 //
 // The bytes bound it: rows in 16 bits are read once, codes and rotated queries
 // written once.  MI355X, prompts of 17 k tokens, 40 query and 8 kv heads of 128:
-// 101 us, 145 MB read and 225 MB written by the counters, 3.7 TB/s.  The queries
-// of a token are turned by one workgroup, its angles held over its heads; that
-// and reading back by 128-byte pieces took the pair from 217 to 136 us.
+// 97 to 105 us, 145 MB read and 225 MB written by the counters, 3.7 TB/s.  The
+// queries of a token are turned by one workgroup, its angles held over its heads;
+// that and reading back by 128-byte pieces took the pair from 217 to 136 us.
 template <int DT, int D, int PASSES>
 __device__ void append_page(const Kv8& c, const Rope& rope, const uint16_t* x, int64_t stride,
                             bool values, int b, int chunk, int head, uint8_t* lds,

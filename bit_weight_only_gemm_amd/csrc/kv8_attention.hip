@@ -161,8 +161,8 @@ __device__ __forceinline__ float four_rows_max(float x) {
 // nor probabilities pass through LDS.
 //
 // The cache's bytes bound it where there are many: 64 ragged sequences of up to
-// 8192 tokens, 40 / 8 heads of 128, 136 us, 5.1 TB/s of codes (MI355X; a plain
-// read gets 5.7); 3 of up to 131001, 119 us.  Few tokens are a chain of waits
+// 8192 tokens, 40 / 8 heads of 128, 139 us, 5.0 TB/s of codes (MI355X; a plain
+// read gets 5.7); 3 of up to 131001, 113 us.  Few tokens are a chain of waits
 // (length, table, keys, values, join): one sequence of 777, 32 heads, 10.3 us.
 // With 16 rows to a wave and not more, three waves share a SIMD and cover each
 // other's waits: 32 or 48 rows a wave read the codes less often, and took 27 us
@@ -476,9 +476,9 @@ __device__ __forceinline__ int swizzle(int row) {
 // The matrix and the vector unit share the time: a unit of 64 tokens costs a
 // wave 2 D / 16 products of 32 cycles, and some 600 vector operations for its
 // probabilities.  MI355X, 4 sequences of 2048 new over 8192, D = 128: 40 / 8 heads
-// 1391 us (865 TFLOP/s), 32 / 32 heads 918 TFLOP/s, matrix units busy 46 %;
-// D = 64: 678 TFLOP/s.  Ragged chunks of up to 2048 over up to 8192 take 1065 us,
-// 2161 in the decode kernel's form.
+// 1247 us (965 TFLOP/s), 32 / 32 heads 953 TFLOP/s, D = 64: 694 TFLOP/s (random
+// codes).  Ragged chunks of up to 2048 over up to 8192 (normal keys and values) take
+// 1076 us, matrix units busy 46 %, and 2161 in the decode kernel's form.
 //
 // WHOLE: pages of 64 tokens and more, a unit lies in one page.
 template <int D>

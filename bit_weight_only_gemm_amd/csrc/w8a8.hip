@@ -357,9 +357,9 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 //    reaches only after these results.
 //
 // The matrix units bound it, at the clock the card holds under them: 8192 x
-// 55296 x 5120 in 1850 us, 2.5 PFLOP/s, the units busy 69 % of the cycles (2.57
-// with every load from L2, 2.82 without loads; with one tile per workgroup and
-// loads straight to LDS it took 2324 us).
+// 55296 x 5120 in 1850 to 1950 us by card, 2.5 to 2.4 PFLOP/s, the units busy 68 %
+// of the cycles (2.57 with every load from L2, 2.82 without loads; with one tile
+// per workgroup and loads straight to LDS it took 2324 us).
 constexpr int kWideStage = 512 * 128, kWideTurn = 2 * kWideStage, kWideScales = kWideTurn + 4 * 4096;
 // x's scales, w's, the bias as fp32; of this tile and of the one before
 constexpr int kWideLds = kWideScales + 2 * 256 * 12;
