@@ -53,6 +53,19 @@ def _need(t, dtype, name, numel=None):
         raise ValueError("%s has %d elements, expected %d" % (name, t.numel(), numel))
 
 
+def _here(stream, *tensors):
+    """Refuses tensors (None: an argument not given) and a stream of another
+    device than the current one, on which the kernels are launched."""
+    now = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != now:
+            raise ValueError("a tensor on device %d, but the current device is %d"
+                             % (t.get_device(), now))
+    if stream is not None and stream.device_index != now:
+        raise ValueError("a stream of device %d, but the current device is %d"
+                         % (stream.device_index, now))
+
+
 def version():
     return _lib.lib().w4a16_version()
 
@@ -383,4 +396,6 @@ def _ws_cache(device, nbytes, stream=None, kept=None):
 
 from .kv8 import (kv8_append, kv8_attention, kv8_attention_workspace_bytes,  # noqa: E402,F401
                   kv8_cache, kv8_dequant)
+from .kv8_pages import (kv8_compact, kv8_copy_pages, kv8_fork, kv8_free,  # noqa: E402,F401
+                        kv8_pages_workspace_bytes, kv8_refs, kv8_reserve)
 from .w8a8 import w8a8_gemm, w8a8_linear, w8a8_quantize, w8a8_workspace_bytes  # noqa: E402,F401

@@ -644,6 +644,83 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
                   int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
                   int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------- pages of the 8-bit cache --- */
+
+/*
+ * Pages of caches in the layout above, shared between the rows of one page
+ * table (sequences, or beams of one) and moved, all on the device: nothing is
+ * read back, and every call can be captured.  The state is
+ *   refs       int32 [num_pages]: rows that hold the page, 0 where it is free
+ *   page_table int32 [B][max_pages], row b's first ceil(seq_lens[b] / T) entries
+ *   seq_lens   int32 [B], 0 for a row that holds nothing
+ * and is the same for `count` caches (the layers of a model), whose arrays are
+ * caches_host: 4 * count device pointers in host memory, k, v, k_scale and
+ * v_scale of each, read before the call returns.  Free pages are taken from
+ * the lowest on, in the order of the rows: results do not depend on timing.
+ * Table entries out of [0, num_pages) are neither counted nor copied; a
+ * length past the table's row counts as the whole row, one below 0 as 0.
+ *   status     int32 [1], device, written by the call: 0 done; above 0 the
+ *              pages that were missing; -1 refused rows.  Unless 0 the call
+ *              has changed nothing else.
+ *   workspace  kv8_pages_workspace_bytes(num_pages, B, n) bytes, n of kv8_fork
+ *              (else 0); its contents need not be initialized.  Calls that
+ *              overlap in time must not share one.
+ * Limits (W4A16_ERR_UNSUPPORTED): num_pages <= 2^30, B <= 2^20, n <= 2^20,
+ * max_pages * T <= 2^30, count <= 65536, Hkv <= 1024.
+ */
+int64_t kv8_pages_workspace_bytes(int64_t num_pages, int64_t B, int64_t n);
+
+/*
+ * Copies pages src[i] over pages dst[i] (int32 [n], device; codes and scales).
+ * Pairs with a page out of range are passed over.  No dst may be named twice or
+ * be a src: such pages are left with parts of either.
+ */
+int kv8_copy_pages(void* const* caches_host, int32_t count, int64_t num_pages, int32_t page_size,
+                   int32_t Hkv, int32_t D, const int32_t* src, const int32_t* dst, int64_t n,
+                   void* stream);
+
+/*
+ * Gives back the pages of table rows rows[0 .. n - 1] (int32, device): refs go
+ * down, entries become -1, lengths 0.  A row out of range is passed over, one
+ * named twice is given back once.  B or n of 0 launches nothing.
+ */
+int kv8_free(int32_t* refs, int64_t num_pages, int32_t page_size, int32_t* page_table,
+             int64_t max_pages, int32_t* seq_lens, int64_t B, const int32_t* rows, int64_t n,
+             void* stream);
+
+/*
+ * Room for added[b] (int32 [B], device; below 0 as 0) more tokens in every row:
+ * the pages they need are taken, and seq_lens become the lengths with them.
+ * status -1: a row would pass max_pages * T.
+ */
+int kv8_reserve(int32_t* refs, int64_t num_pages, int32_t page_size, int32_t* page_table,
+                int64_t max_pages, int32_t* seq_lens, int64_t B, const int32_t* added,
+                int32_t* status, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Makes row dst[i] a copy of row src[i] (int32 [n], device): its whole pages
+ * are shared, a partly filled last page is copied to a page taken for it, so
+ * that both rows may append.  Entries past those keep their values.  status -1:
+ * a row is out of range, or a dst is not empty, named twice or a src.
+ */
+int kv8_fork(void* const* caches_host, int32_t count, int64_t num_pages, int32_t page_size,
+             int32_t Hkv, int32_t D, int32_t* refs, int32_t* page_table, int64_t max_pages,
+             int32_t* seq_lens, int64_t B, const int32_t* src, const int32_t* dst, int64_t n,
+             int32_t* status, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Moves the pages in use to the beginning of the pool: used (int32 [1], device)
+ * = their count; those from page `used` on go to the free pages below it, both
+ * ascending.  refs_out and page_table_out are written whole and may be refs and
+ * page_table themselves (and may not overlap them otherwise).  Pages moved from
+ * keep their bytes: work that goes by the old table stays right until they are
+ * taken again.
+ */
+int kv8_compact(void* const* caches_host, int32_t count, int64_t num_pages, int32_t page_size,
+                int32_t Hkv, int32_t D, int32_t* refs, int32_t* refs_out, int32_t* page_table,
+                int32_t* page_table_out, int64_t max_pages, const int32_t* seq_lens, int64_t B,
+                int32_t* used, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
