@@ -177,6 +177,68 @@ __device__ __forceinline__ u32x2_t results4(const i32x16_t& acc, int g, float s,
   return u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
 }
 
+// ------------------------------------------------------ gated product (ACT) ---
+// Gated kernels take w as 2 F rows, the gate's and then the up projection's, and
+// form F channels y = act(g) u.  They go through w's rows in blocks of 8, the
+// gate's and the up projection's in turn, so that a lane whose results are
+// channels 8 i + 4 h + e of the gate has the same channels of the up projection in
+// its next four registers, whatever the tile; N counts all 2 F rows.
+//
+// act(g) = g sigmoid(a g + b g^3) for silu (a = 1, b = 0) and for gelu in its tanh
+// form (0.5 (1 + tanh z) = sigmoid(2 z)); log2 e is in a and b.  gelu is g Phi(g),
+// with Phi(-y) = exp(-y^2 / 2) P(1 / (1 + 0.35 y)), y >= 0: P is a fit of degree 7 to
+// erfcx(y / sqrt 2) / 2 over [0, 14.5], 5e-7 off (7e-7 in fp32), and both of its tails
+// keep that relative error.  g, u and act are fp32 and rounded once, as y.
+enum { kNoGate = 0, kSigmoid = 1, kErf = 2 };
+struct Gate {
+  int F;
+  float a, b;
+};
+template <int ACT>
+__device__ __forceinline__ float gated(float g, float u, const Gate& c) {
+  if constexpr (ACT == kSigmoid) {
+    const float w = g * __builtin_fmaf(c.b, fminf(g * g, 3e38f), c.a);
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-w)) * u;
+  } else {
+    const float y = fabsf(g), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.35f, y, 1.0f));
+    float p = 0.04819544777f;
+    p = __builtin_fmaf(p, t, -0.19929255545f);
+    p = __builtin_fmaf(p, t, 0.23627594113f);
+    p = __builtin_fmaf(p, t, -0.01347748376f);
+    p = __builtin_fmaf(p, t, 0.15433320403f);
+    p = __builtin_fmaf(p, t, 0.13377590477f);
+    p = __builtin_fmaf(p, t, 0.14021381736f);
+    p = __builtin_fmaf(p, t, -0.00002427048f);
+    p *= __builtin_amdgcn_exp2f(y * (y * -0.72134752044f));
+    return g * (g < 0.0f ? p : 1.0f - p) * u;
+  }
+}
+
+// gated() of results 8 p .. 8 p + 3 of a product (the gate's) and the 4 after.
+template <int DT, int ACT>
+__device__ __forceinline__ u32x2_t gated4(const i32x16_t& acc, int p, float s, float4_t tg,
+                                          float4_t bg, float4_t tu, float4_t bu, const Gate& c) {
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    y[e] = gated<ACT>(result(acc[8 * p + e], s, tg[e], bg[e]),
+                      result(acc[8 * p + 4 + e], s, tu[e], bu[e]), c);
+  return u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
+}
+
+// Scales and bias of the 4 channels from n on.
+template <int DT>
+__device__ __forceinline__ void channels4(const float* sw, const uint16_t* bias, int64_t n,
+                                          float4_t& t, float4_t& b) {
+  t = *(const float4_t*)(sw + n);
+  b = float4_t{0, 0, 0, 0};
+  if (bias) {
+    const u32x2_t w = *(const u32x2_t*)(bias + n);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = widen16<DT>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+  }
+}
+
 // Tile shape: WM x WN waves, each MT x NT products of 32 x 32.
 template <int MT_, int NT_, int WM_, int WN_, int NS_>
 struct Tile {
@@ -207,12 +269,12 @@ struct Tile {
 // 333 x 7168 x 5120 in 23.3 us (1.05 PFLOP/s; 25.1 with 4 waves of 2 x 2, 22.8
 // with 16 of 1 x 1, 24.0 with 96 x 128 tiles; reading operands two quarters
 // ahead changed nothing), 128 x 4096 x 4096 in 64 x 64 tiles 11.3 us.
-template <int DT, class TL>
+template <int DT, class TL, int ACT>
 __global__ void __launch_bounds__(64 * TL::WAVES)
 w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
                  const int8_t* __restrict__ wq, const float* __restrict__ sw,
                  const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
-                 int K, int mb, int nb, int per_xcd) {
+                 int K, int mb, int nb, int per_xcd, Gate gate) {
   constexpr int MT = TL::MT, NT = TL::NT, NS = TL::NS, L = TL::LOADS;
   __shared__ __attribute__((aligned(16))) uint8_t lds[NS * TL::STAGE];
   // ---- tile of this workgroup: workgroups go to the 8 XCDs in turn, so each
@@ -227,7 +289,11 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / TL::WN, wn = wave % TL::WN;
   const int KT = (K + 127) >> 7;
-  const rsrc_t rw = make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(TL::BN, N - col0) * (uint32_t)K);
+  // (gated: rw the gate's rows, ru the up projection's)
+  constexpr int HALVES = ACT ? 2 : 1;
+  const uint32_t w_bytes = (uint32_t)min(TL::BN, N - col0) / HALVES * (uint32_t)K;
+  const rsrc_t rw = make_rsrc(wq + (size_t)(col0 / HALVES) * K, w_bytes);
+  const rsrc_t ru = ACT ? make_rsrc(wq + (size_t)(gate.F + col0 / HALVES) * K, w_bytes) : rw;
   const rsrc_t rx = make_rsrc(xq + (size_t)row0 * K, (uint32_t)min(TL::BM, M - row0) * (uint32_t)K);
 
   // load i of this wave fills the LDS block WAVES i + wave (8 rows); blocks
@@ -238,9 +304,11 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     const bool is_w = blk < TL::BN / 8;
     const uint32_t row = 8u * (uint32_t)(is_w ? blk : blk - TL::BN / 8) + (uint32_t)lrow;
     const uint32_t chunk = ((uint32_t)lane & 7u) ^ ((row >> 1) & 7u);
+    const uint32_t from = ACT && is_w ? 8u * (uint32_t)(blk >> 1) + (uint32_t)lrow : row;
     const uint32_t off =
-        128 * t + 16 * (int)chunk < K ? row * (uint32_t)K + 16u * chunk : kOutOfRange;
-    dma16(is_w ? rw : rx, lds + (t % NS) * TL::STAGE + blk * 1024, off, t * 128);
+        128 * t + 16 * (int)chunk < K ? from * (uint32_t)K + 16u * chunk : kOutOfRange;
+    dma16(!is_w ? rx : ACT && (blk & 1) ? ru : rw, lds + (t % NS) * TL::STAGE + blk * 1024, off,
+          t * 128);
   };
 
   const int r = lane & 31, h = lane >> 5;
@@ -300,10 +368,10 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 
   // ---- results: register i of product (nt, mt) is channel 8 (i >> 2) + 4 h +
   // (i & 3) of its 32, token lane & 31; one 32-token block of the wave at a time
-  constexpr int ROW = NT * 64 + 16;  // bytes of a token's row in LDS
+  constexpr int ROW = NT * 64 / HALVES + 16;  // bytes of a token's row in LDS
   static_assert(TL::WAVES * 32 * ROW <= NS * TL::STAGE, "the results fit");
   uint8_t* mine = lds + wave * 32 * ROW;
-  const int wcol = col0 + wn * NT * 32;
+  const int width = N / HALVES, wcol = (col0 + wn * NT * 32) / HALVES;  // of y
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int mrow = row0 + (wm * MT + j) * 32;
@@ -311,27 +379,27 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int n = wcol + i * 32 + 8 * g + 4 * h;
+      for (int g = 0; g < 4 / HALVES; ++g) {
+        const int n = wcol + i * (32 / HALVES) + 8 * g + 4 * h;
         float4_t t = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-        if (n < N) {
-          t = *(const float4_t*)(sw + n);
-          if (bias) {
-            const u32x2_t w = *(const u32x2_t*)(bias + n);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              b[e] = widen16<DT>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-          }
+        if (n < width) channels4<DT>(sw, bias, n, t, b);
+        uint8_t* to = mine + r * ROW + i * (64 / HALVES) + 16 * g + 8 * h;
+        if constexpr (ACT != kNoGate) {
+          float4_t tu = {0, 0, 0, 0}, bu = {0, 0, 0, 0};
+          if (n < width) channels4<DT>(sw, bias, (int64_t)gate.F + n, tu, bu);
+          *(u32x2_t*)to = gated4<DT, ACT>(acc[i][j], g, s, t, b, tu, bu, gate);
+        } else {
+          *(u32x2_t*)to = results4<DT>(acc[i][j], g, s, t, b);
         }
-        *(u32x2_t*)(mine + r * ROW + i * 64 + 16 * g + 8 * h) = results4<DT>(acc[i][j], g, s, t, b);
       }
-    constexpr int LR = NT * 4;  // lanes per row
+    constexpr int LR = NT * 4 / HALVES;  // lanes per row
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int k = 0; k < 32 / (64 / LR); ++k) {
       const int tr = k * (64 / LR) + lane / LR, c = (lane % LR) * 8;
       const u32x4_t v = *(const u32x4_t*)(mine + tr * ROW + c * 2);
-      if (mrow + tr < M && wcol + c < N) *(u32x4_t*)(out + (size_t)(mrow + tr) * N + wcol + c) = v;
+      if (mrow + tr < M && wcol + c < width)
+        *(u32x4_t*)(out + (size_t)(mrow + tr) * width + wcol + c) = v;
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -364,12 +432,13 @@ constexpr int kWideStage = 512 * 128, kWideTurn = 2 * kWideStage, kWideScales = 
 // x's scales, w's, the bias as fp32; of this tile and of the one before
 constexpr int kWideLds = kWideScales + 2 * 256 * 12;
 
-template <int DT>
+template <int DT, int ACT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
                  const int8_t* __restrict__ wq, const float* __restrict__ sw,
                  const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
-                 int K, int mb, int nb, int per_xcd) {
+                 int K, int mb, int nb, int per_xcd, Gate gate) {
+  constexpr int HALVES = ACT ? 2 : 1;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWideLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -393,23 +462,30 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   // ---- loads: instruction i of a step fetches 8 rows x 128 bytes, i < 8 rows
   // of w and i >= 8 rows of x, of rows 64 wave + 8 (i & 7) of the tile
   const int lrow = lane >> 3, lchunk = lane & 7;
+  // (gated: block 8 wave + i of w is the block (8 wave + i) / 2 of the gate's rows
+  // where i is even, of the up projection's where it is odd)
   const uint32_t lane_off = (uint32_t)(64 * wave + lrow) * (uint32_t)K + 16u * lchunk;
+  const uint32_t gate_off = (uint32_t)(32 * wave + lrow) * (uint32_t)K + 16u * lchunk;
   const uint32_t tail = 128 * (KT - 1) + 16 * lchunk >= K ? kOutOfRange : 0u;
   const uint32_t lane_lds = (uint32_t)(64 * wave + lrow) * 128 + 16u * (lchunk ^ ((lrow >> 1) & 3));
   int lat = first, lt = 0;  // the step that is loaded next
-  rsrc_t rw, rx;
+  rsrc_t rw, ru, rx;
   auto aim = [&]() {
     int row0 = 0, col0 = 0;
     const bool any = lat < run1;
     if (any) tile_at(lat, row0, col0);
-    rw = make_rsrc(wq + (size_t)col0 * K, any ? (uint32_t)min(256, N - col0) * (uint32_t)K : 0u);
+    const uint32_t w_bytes = any ? (uint32_t)min(256, N - col0) / HALVES * (uint32_t)K : 0u;
+    rw = make_rsrc(wq + (size_t)(col0 / HALVES) * K, w_bytes);
+    if constexpr (ACT != kNoGate) ru = make_rsrc(wq + (size_t)(gate.F + col0 / 2) * K, w_bytes);
     rx = make_rsrc(xq + (size_t)row0 * K, any ? (uint32_t)min(256, M - row0) * (uint32_t)K : 0u);
   };
   aim();
   i32x4_t held[16];
   auto load = [&](int i) {
-    const uint32_t off = (lane_off + (uint32_t)(8 * (i & 7)) * (uint32_t)K) | (lt == KT - 1 ? tail : 0u);
-    held[i] = __builtin_bit_cast(i32x4_t, bld128(i < 8 ? rw : rx, off, lt * 128));
+    const bool half = ACT && i < 8;
+    const uint32_t row = half ? 8 * (i >> 1) : 8 * (i & 7);
+    const uint32_t off = ((half ? gate_off : lane_off) + row * (uint32_t)K) | (lt == KT - 1 ? tail : 0u);
+    held[i] = __builtin_bit_cast(i32x4_t, bld128(i >= 8 ? rx : half && (i & 1) ? ru : rw, off, lt * 128));
   };
   auto loaded = [&]() {  // every load of a step is out
     if (++lt == KT) {
@@ -506,8 +582,11 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     int row0, col0;
     tile_at(at, row0, col0);
     sx_v = row0 + tid < M ? sx[row0 + tid] : 0.0f;
-    sw_v = col0 + tid < N ? sw[col0 + tid] : 0.0f;
-    bias_v = bias && col0 + tid < N ? widen16<DT>(bias[col0 + tid]) : 0.0f;
+    // (the channel of w's row tid of the tile)
+    const int64_t ch = ACT ? (int64_t)col0 / 2 + (tid >> 4) * 8 + (tid & 7) + (tid & 8 ? gate.F : 0)
+                           : col0 + tid;
+    sw_v = col0 + tid < N ? sw[ch] : 0.0f;
+    bias_v = bias && col0 + tid < N ? widen16<DT>(bias[ch]) : 0.0f;
     step(std::true_type{});
     for (int t = 1; t < KT; ++t) step(std::false_type{});
     // the sums stay in accumulation registers until their block's turn
@@ -517,41 +596,45 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
       for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
 
     // ---- results: register e of product (i, j) is channel 8 (e >> 2) + 4 h +
-    // (e & 3) of its 32, token lane & 31; blocks of 32 tokens x 64 channels, the
+    // (e & 3) of its 32, token lane & 31; blocks of 32 tokens x 64 channels of y, the
     // 16-byte chunk c of token r at position c ^ (r & 7)
-    const int wcol = col0 + wn * 128;
+    const int width = N / HALVES, wcol = (col0 + wn * 128) / HALVES;
     // (hidden from the compiler, which would keep every address of this part
     // in registers all through the steps, and spill)
     int at_lane = lane;
     asm volatile("" : "+v"(at_lane));
     const int r = at_lane & 31, h = at_lane >> 5;
 #pragma unroll
-    for (int i0 = 0; i0 < 4; i0 += 2) {
+    for (int i0 = 0; i0 < 4; i0 += 2 * HALVES) {
       const float* sn = scales_at(256 + wn * 128 + i0 * 32 + 4 * h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int mrow = row0 + (wm * 4 + j) * 32;
         const float s = *scales_at((wm * 4 + j) * 32 + r);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2 * HALVES; ++i)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < 4 / HALVES; ++g) {
             // (the scales are read again for each block of tokens: held, they
             // would cost the registers that the next tile's rows wait in)
-            const float4_t t = *(const float4_t*)(sn + i * 32 + 8 * g);
-            const float4_t b = *(const float4_t*)(sn + 256 + i * 32 + 8 * g);
-            *(u32x2_t*)(mine + r * 128 + (((i * 4 + g) ^ (r & 7)) << 4) + 8 * h) =
-                results4<DT>(acc[i0 + i][j], g, s, t, b);
+            const float* sg = sn + i * 32 + 8 * HALVES * g;
+            const float4_t t = *(const float4_t*)sg, b = *(const float4_t*)(sg + 256);
+            uint8_t* to = mine + r * 128 + (((i * (4 / HALVES) + g) ^ (r & 7)) << 4) + 8 * h;
+            if constexpr (ACT != kNoGate)
+              *(u32x2_t*)to = gated4<DT, ACT>(acc[i0 + i][j], g, s, t, b, *(const float4_t*)(sg + 8),
+                                              *(const float4_t*)(sg + 264), gate);
+            else
+              *(u32x2_t*)to = results4<DT>(acc[i0 + i][j], g, s, t, b);
           }
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_wave_barrier();
-        const int c = at_lane & 7, n = wcol + i0 * 32 + c * 8;
+        const int c = at_lane & 7, n = wcol + i0 * 32 / HALVES + c * 8;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int tr = k * 8 + (at_lane >> 3);
           const u32x4_t v = *(const u32x4_t*)(mine + tr * 128 + ((c ^ (tr & 7)) << 4));
-          if (mrow + tr < M && n < N)
-            *(u32x4_t*)(out + (size_t)(mrow + tr) * N + n) = v;
+          if (mrow + tr < M && n < width)
+            *(u32x4_t*)(out + (size_t)(mrow + tr) * width + n) = v;
         }
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_wave_barrier();
@@ -574,12 +657,15 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 // 8 values of up to kRows rows of 4096 (a longer row counts as several).
 constexpr int kRows = 4;
 
-template <int DT, int MB, int NT, bool FUSED, int AHEAD>
+//
+// Gated, w is one buffer (less than 4 GB): 8 of the 16 rows of a product are the
+// gate's, 8 the up projection's.
+template <int DT, int MB, int NT, bool FUSED, int AHEAD, int ACT>
 __global__ void __launch_bounds__(512)
 w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __restrict__ sx,
                    const int8_t* __restrict__ wq, const float* __restrict__ sw,
                    const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
-                   int K) {
+                   int K, Gate gate) {
   constexpr int kSum = 8 * NT * MB * 1024, kCodes = FUSED ? kRows * 4096 + 16 * 16 : 0;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kSum > kCodes ? kSum : kCodes];
   __shared__ uint32_t mags[FUSED ? kRows : 1][8];
@@ -589,8 +675,11 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
   const int r = lane & 15, g = lane >> 4;
   const int col0 = (int)blockIdx.x * 16 * NT;
   const int KT = (K + 127) >> 7;
-  const rsrc_t rw = make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(16 * NT, N - col0) * (uint32_t)K);
-  const uint32_t lane_off = (uint32_t)r * (uint32_t)K + 16u * g;
+  constexpr int HALVES = ACT ? 2 : 1;
+  const rsrc_t rw = ACT ? make_rsrc(wq, (uint32_t)N * (uint32_t)K)
+                        : make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(16 * NT, N - col0) * (uint32_t)K);
+  const uint32_t lane_row = ACT ? (uint32_t)(col0 / 2 + (r & 7) + (r & 8 ? gate.F : 0)) : (uint32_t)r;
+  const uint32_t lane_off = lane_row * (uint32_t)K + 16u * g;
   auto load_w = [&](int s, i32x4_t (&w)[2][NT]) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -598,8 +687,8 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
       for (int e = 0; e < 2; ++e)
         w[e][i] = __builtin_bit_cast(
             i32x4_t, bld128(rw,
-                            128 * s + 64 * e + 16 * g < K
-                                ? lane_off + (uint32_t)(16 * i) * (uint32_t)K + 64 * e
+                            128 * s + 64 * e + 16 * g < K && (!ACT || col0 + 16 * i < N)
+                                ? lane_off + (uint32_t)(16 / HALVES * i) * (uint32_t)K + 64 * e
                                 : kOutOfRange,
                             s * 128));
   };
@@ -699,18 +788,34 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
 #pragma unroll
     for (int j = 0; j < MB; ++j) part[((wave * NT + i) * MB + j) * 64 + r * 4 + g] = acc[i][j];
   __syncthreads();
-  for (int e = tid; e < NT * MB * 64; e += 512) {
-    const int i = e / (64 * MB), j = e / 64 % MB, m = 16 * j + (e % 64) / 4, n = col0 + 16 * i + 4 * (e % 4);
+  auto sum_of = [&](int e) {
     i32x4_t v = part[e];
 #pragma unroll
     for (int p = 1; p < 8; ++p) v += part[p * NT * MB * 64 + e];
-    if (m < M && n < N) {
+    return v;
+  };
+  // gated: entries 0 and 1 of a token's four are the gate's, 2 and 3 the up projection's
+  for (int at = tid; at < NT * MB * 64 / HALVES; at += 512) {
+    const int e = ACT ? (at >> 1) * 4 + (at & 1) : at;
+    const int i = e / (64 * MB), j = e / 64 % MB, m = 16 * j + (e % 64) / 4;
+    const int n = (col0 + 16 * i) / HALVES + 4 * (e % 4);
+    const i32x4_t v = sum_of(e);
+    if (m < M && n < N / HALVES) {
       const float4_t t = *(const float4_t*)(sw + n);
       float y[4];
 #pragma unroll
       for (int a = 0; a < 4; ++a)
         y[a] = result(v[a], scales[m], t[a], bias ? widen16<DT>(bias[n + a]) : 0.0f);
-      *(u32x2_t*)(out + (size_t)m * N + n) = u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
+      if constexpr (ACT != kNoGate) {
+        const i32x4_t vu = sum_of(e + 2);
+        float4_t tu, bu;
+        channels4<DT>(sw, bias, (int64_t)gate.F + n, tu, bu);
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+          y[a] = gated<ACT>(y[a], result(vu[a], scales[m], tu[a], bu[a]), gate);
+      }
+      *(u32x2_t*)(out + (size_t)m * (N / HALVES) + n) =
+          u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
     }
   }
 }
@@ -729,36 +834,40 @@ struct Args {
   const uint16_t* bias;
   uint16_t* out;
   int M, N, K;
+  Gate gate;  // of the gated kernels
 };
 
-template <int DT, class TL>
+template <int DT, class TL, int ACT>
 void launch_tile(const Args& a, hipStream_t st) {
   const int mb = (int)ceil_div(a.M, TL::BM), nb = (int)ceil_div(a.N, TL::BN);
   const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
-  launch_timed(w8a8_tile_kernel<DT, TL>, dim3((unsigned)per_xcd * 8), dim3(64 * TL::WAVES), 0, st,
-               (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb, per_xcd);
+  launch_timed(w8a8_tile_kernel<DT, TL, ACT>, dim3((unsigned)per_xcd * 8), dim3(64 * TL::WAVES), 0, st,
+               (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb, per_xcd,
+               a.gate);
 }
 
-template <int DT, int MB, int NT, bool FUSED>
+template <int DT, int MB, int NT, bool FUSED, int ACT>
 void launch_stream(const Args& a, hipStream_t st) {
   // rows of w under way per wave: where there is work before they are used,
   // 4 steps in all (1 x 4096 x 4096: 9.1 us with one step, 8.0 with four);
   // otherwise one, whose few registers leave room for a second workgroup
   // (16 x 4096 x 11008: 12.5 us, 13.4 with four; 8 x 5120 x 16384: 28, 30.2)
   constexpr int AHEAD = FUSED ? 4 / NT : 1;
-  launch_timed(w8a8_stream_kernel<DT, MB, NT, FUSED, AHEAD>, dim3((unsigned)ceil_div(a.N, 16 * NT)),
-               dim3(512), 0, st, a.x, a.x_stride, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K);
+  launch_timed(w8a8_stream_kernel<DT, MB, NT, FUSED, AHEAD, ACT>,
+               dim3((unsigned)ceil_div(a.N, 16 * NT)), dim3(512), 0, st, a.x, a.x_stride, a.sx, a.wq,
+               a.sw, a.bias, a.out, a.M, a.N, a.K, a.gate);
 }
 
 // Whether w8a8_linear quantizes inside the product.
 bool fused(int64_t M, int64_t K) { return M * ceil_div(K, 4096) <= kRows; }
 
-template <int DT>
+template <int DT, int ACT>
 void launch_wide(const Args& a, hipStream_t st) {
   const int mb = (int)ceil_div(a.M, 256), nb = (int)ceil_div(a.N, 256);
   const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
-  launch_timed(w8a8_wide_kernel<DT>, dim3((unsigned)std::min(256, per_xcd * 8)), dim3(256), 0, st,
-               (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb, per_xcd);
+  launch_timed(w8a8_wide_kernel<DT, ACT>, dim3((unsigned)std::min(256, per_xcd * 8)), dim3(256), 0, st,
+               (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb, per_xcd,
+               a.gate);
 }
 
 // The kernel of a call.  A kernel's time per step of 128 codes was measured on
@@ -776,7 +885,7 @@ void launch_wide(const Args& a, hipStream_t st) {
 //   16 x 4096 x 11008 12.5 / 24.6, 16 x 8192 x 4096 11.2 / 11.8,
 //   16 x 12288 x 4096 14.7 / 12.0, 32 x 4096 x 4096 8.8 / 11.6,
 //   32 x 8192 x 4096 14.5 / 11.7, 64 x 4096 x 4096 12.5 / 12.0
-template <int DT>
+template <int DT, int ACT>
 hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
   const int64_t t64 = ceil_div(a.M, 64) * ceil_div(a.N, 64);
   const int64_t t128 = ceil_div(a.M, 128) * ceil_div(a.N, 128);
@@ -784,15 +893,15 @@ hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
   const int64_t c64 = 3 * std::max<int64_t>(t64, 256), c128 = 6 * 256 * ceil_div(t128, 256),
                 c256 = 16 * 256 * ceil_div(t256, 256);
   if (a.M <= 64 && ceil_div(a.M, 16) * a.N < 12288) {
-    if (a.M > 32) launch_stream<DT, 4, 1, false>(a, st);
-    else if (a.M > 16) launch_stream<DT, 2, 1, false>(a, st);
-    else launch_stream<DT, 1, 1, false>(a, st);
+    if (a.M > 32) launch_stream<DT, 4, 1, false, ACT>(a, st);
+    else if (a.M > 16) launch_stream<DT, 2, 1, false, ACT>(a, st);
+    else launch_stream<DT, 1, 1, false, ACT>(a, st);
   } else if (c64 <= c128 && c64 <= c256) {
-    launch_tile<DT, T64>(a, st);
+    launch_tile<DT, T64, ACT>(a, st);
   } else if (c128 <= c256) {
-    launch_tile<DT, T128>(a, st);
+    launch_tile<DT, T128, ACT>(a, st);
   } else {
-    launch_wide<DT>(a, st);
+    launch_wide<DT, ACT>(a, st);
   }
   return hipGetLastError();
 }
@@ -800,26 +909,42 @@ hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
 hipError_t launch_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                        const void* bias, void* out, int64_t M, int64_t N, int64_t K, int dtype,
                        hipStream_t st) {
-  const Args a = {xq, K, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K};
-  return (dtype == DT_F16 ? launch_gemm_dt<DT_F16> : launch_gemm_dt<DT_BF16>)(a, st);
+  const Args a = {xq, K, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K, {}};
+  return (dtype == DT_F16 ? launch_gemm_dt<DT_F16, kNoGate> : launch_gemm_dt<DT_BF16, kNoGate>)(a, st);
 }
 
 // Channels per workgroup: 64 where that leaves two workgroups for each of 256
 // CUs, else 32, else 16 (each reads and quantizes the tokens for itself).
-template <int DT>
+template <int DT, int ACT>
 void launch_fused_dt(const Args& a, hipStream_t st) {
-  if (a.N >= 512 * 64) launch_stream<DT, 1, 4, true>(a, st);
-  else if (a.N >= 512 * 32) launch_stream<DT, 1, 2, true>(a, st);
-  else launch_stream<DT, 1, 1, true>(a, st);
+  if (a.N >= 512 * 64) launch_stream<DT, 1, 4, true, ACT>(a, st);
+  else if (a.N >= 512 * 32) launch_stream<DT, 1, 2, true, ACT>(a, st);
+  else launch_stream<DT, 1, 1, true, ACT>(a, st);
 }
 
 hipError_t launch_fused(const void* x, int64_t x_stride, const int8_t* wq, const float* sw,
                         const void* bias, void* out, int64_t M, int64_t N, int64_t K, int dtype,
                         hipStream_t st) {
   const Args a = {x, x_stride, nullptr, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M,
-                  (int)N, (int)K};
-  (dtype == DT_F16 ? launch_fused_dt<DT_F16> : launch_fused_dt<DT_BF16>)(a, st);
+                  (int)N, (int)K, {}};
+  (dtype == DT_F16 ? launch_fused_dt<DT_F16, kNoGate> : launch_fused_dt<DT_BF16, kNoGate>)(a, st);
   return hipGetLastError();
+}
+
+// Whether w8a8_gated quantizes inside the product: where w8a8_linear does and w
+// is one buffer.
+bool fused_gated(int64_t M, int64_t F, int64_t K) {
+  return fused(M, K) && 2 * F * K < ((int64_t)1 << 32);
+}
+
+// A gated call on 16-bit rows (sx null) or on codes.
+template <int DT>
+hipError_t launch_gated(const Args& a, int act, hipStream_t st) {
+  if (a.sx == nullptr) {
+    (act == W4A16_GELU ? launch_fused_dt<DT, kErf> : launch_fused_dt<DT, kSigmoid>)(a, st);
+    return hipGetLastError();
+  }
+  return (act == W4A16_GELU ? launch_gemm_dt<DT, kErf> : launch_gemm_dt<DT, kSigmoid>)(a, st);
 }
 
 // --------------------------------------------------------------- checking ---
@@ -894,6 +1019,43 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
     float* sx = (float*)(xq + pad256(M * K));
     if (int s = hip_status(launch_quantize(x, M, K, x_stride, dtype, xq, sx, st))) return s;
     return hip_status(launch_gemm(xq, sx, wq, w_scale, bias, out, M, N, K, dtype, st));
+  });
+}
+
+int64_t w8a8_gated_workspace_bytes(int64_t M, int64_t F, int64_t K) {
+  if (F <= 0 || F > kMaxN || F % 8 != 0 || validate_shape(M, 2 * F, K) != W4A16_OK) return -1;
+  return fused_gated(M, F, K) ? 0 : linear_bytes(M, K);
+}
+
+int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w_scale,
+               const void* bias, int32_t act, void* out, int64_t M, int64_t F, int64_t K,
+               int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    if (F <= 0 || F % 8 != 0) return W4A16_ERR_INVALID_ARG;
+    if (F > kMaxN) return W4A16_ERR_UNSUPPORTED;
+    if (int s = validate_shape(M, 2 * F, K)) return s;
+    if (int s = validate_dtype(dtype)) return s;
+    if (act < W4A16_SILU || act > W4A16_GELU_TANH) return W4A16_ERR_INVALID_ARG;
+    if (x_stride < K || x_stride % 8 != 0) return W4A16_ERR_INVALID_ARG;
+    if (int s = check_ptrs({x, wq, w_scale, out})) return s;
+    if (!aligned16(bias) || !aligned16(workspace)) return W4A16_ERR_MISALIGNED;
+    const int64_t need = w8a8_gated_workspace_bytes(M, F, K);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+    clear_pending_error();
+    const hipStream_t st = (hipStream_t)stream;
+    // sigmoid(a g + b g^3): 1 and 0, or 2 sqrt(2 / pi) (1 and 0.044715); times log2 e
+    const float log2e = 1.4426950408889634f;
+    const float a1 = act == W4A16_SILU ? log2e : 1.5957691216057308f * log2e;
+    Args a = {x, x_stride, nullptr, wq, w_scale, (const uint16_t*)bias, (uint16_t*)out, (int)M,
+              (int)(2 * F), (int)K, {(int)F, a1, act == W4A16_SILU ? 0.0f : 0.044715f * a1}};
+    if (!fused_gated(M, F, K)) {
+      int8_t* xq = (int8_t*)workspace;
+      float* sx = (float*)(xq + pad256(M * K));
+      if (int s = hip_status(launch_quantize(x, M, K, x_stride, dtype, xq, sx, st))) return s;
+      a.x = xq;
+      a.sx = sx;
+    }
+    return hip_status((dtype == DT_F16 ? launch_gated<DT_F16> : launch_gated<DT_BF16>)(a, act, st));
   });
 }
 

@@ -4,6 +4,8 @@
     wq, ws = w8a8_quantize(W)                  # once per layer, W [N, K]
     y = w8a8_linear(x, wq, ws)                 # x [M, K] fp16/bf16, quantized per token
 
+    y = w8a8_gated(x, wq, ws, act="silu")      # W [2 F, K], gate and up: [M, F]
+
 or, for rows quantized once and used by several layers:
 
     xq, xs = w8a8_quantize(x)
@@ -12,10 +14,11 @@ or, for rows quantized once and used by several layers:
 
 import torch
 
-from . import _DT, _lib, _need, _stream, _ws_cache
+from . import _DT, _here, _lib, _need, _stream, _ws_cache
 
 _QDT = dict(_DT)
 _QDT[torch.float32] = 2
+_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
 def _empty(shape, dtype, device, stream=None):
@@ -143,4 +146,39 @@ def w8a8_linear(x, wq, w_scale, bias=None, out=None, workspace=None, stream=None
                            _stream(stream))
     if status:
         _lib.check(status, "w8a8_linear")
+    return out
+
+
+def w8a8_gated_workspace_bytes(M, F, K):
+    """Bytes that w8a8_gated needs at this shape."""
+    n = int(_lib.lib().w8a8_gated_workspace_bytes(M, F, K))
+    if n < 0:
+        raise _lib.W4A16Error("w8a8_gated_workspace_bytes: invalid shape M=%d F=%d K=%d" % (M, F, K))
+    return n
+
+
+def w8a8_gated(x, wq, w_scale, bias=None, act="silu", out=None, workspace=None, stream=None):
+    """y = act(x @ Wg^T + bg) * (x @ Wu^T + bu) in one kernel, for x [..., K]
+    fp16/bf16 quantized per row on the way: [..., F].  wq int8 [2 F, K], w_scale
+    and bias [2 F] hold the gate's rows and then the up projection's.  act:
+    "silu", "gelu" (with the error function) or "gelu_tanh".  workspace: one of
+    w8a8_gated_workspace_bytes (kept per stream when not given); it is written
+    over, so never kv8_attention's, and calls that overlap in time (graphs
+    replayed side by side) must not share one."""
+    if act not in _ACT:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(_ACT), act))
+    N, K = _weights(wq, w_scale, bias, x.dtype)
+    if N % 2:
+        raise ValueError("wq must be [2 F, K], got %d rows" % N)
+    M, _, stride = _rows(x, _DT, "x", K)
+    _here(stream, x, wq, w_scale, bias, out, workspace)
+    F, dtype = N // 2, x.dtype
+    out = _output(out, (*x.shape[:-1], F), dtype, x.device, stream)
+    L = _lib.lib()
+    workspace, nbytes = _space(workspace, L.w8a8_gated_workspace_bytes(M, F, K), x.device, stream)
+    status = L.w8a8_gated(x.data_ptr(), stride, wq.data_ptr(), w_scale.data_ptr(), _at(bias),
+                          _ACT[act], out.data_ptr(), M, F, K, _DT[dtype], _at(workspace), nbytes,
+                          _stream(stream))
+    if status:
+        _lib.check(status, "w8a8_gated")
     return out

@@ -533,6 +533,30 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
                 const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t dtype,
                 void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * The gated feed-forward product, both projections, the activation and the
+ * product in one kernel, with w8a8_quantize of x (fp16 or bf16, row stride
+ * x_stride) before it or in it:
+ *   y[m, f] = round_dtype(act(g) * u),  g = v[m, f], u = v[m, F + f],
+ *   v[m, n] = fp32(sum_k cx[m, k] cw[n, k]) * (sx[m] * sw[n]) + b[n],
+ * fp32 up to the one rounding.  wq int8 [2 F, K], w_scale fp32 [2 F] and bias
+ * [2 F] (dtype, or NULL) hold the gate's rows and then the up projection's, as
+ * a fused projection has them; out [M, F] in dtype.
+ *   act  W4A16_SILU: g / (1 + exp(-g)); W4A16_GELU: g Phi(g), Phi the normal
+ *        distribution's; W4A16_GELU_TANH: g / 2 (1 + tanh(sqrt(2 / pi) (g +
+ *        0.044715 g^3))).  Each within 2^-19 of itself and 2^-22 for each unit of
+ *        the exponential's argument; below 2^-126 |g| it may be 0.
+ * Constraints and limits as for w8a8_gemm with N = 2 F, F % 8 == 0; the
+ * workspace (codes of x) as for w8a8_linear, by w8a8_gated_workspace_bytes (-1
+ * on bad input).  Async.  Bitwise reproducible, and a row of y does not depend on
+ * the other rows.
+ */
+typedef enum { W4A16_SILU = 0, W4A16_GELU = 1, W4A16_GELU_TANH = 2 } w4a16_act_t;
+int64_t w8a8_gated_workspace_bytes(int64_t M, int64_t F, int64_t K);
+int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w_scale,
+               const void* bias, int32_t act, void* out, int64_t M, int64_t F, int64_t K,
+               int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* -------------------------------------------------- paged cache in 8 bits --- */
 
 /*

@@ -1,0 +1,57 @@
+"""Host-only checks of w8a8_gated: refusals, workspace sizes, and pins of its
+oracle."""
+
+import ctypes
+import math
+import os
+
+import numpy as np
+import pytest
+
+from bit_weight_only_gemm_amd import _lib
+from oracle import w8a8
+
+if not os.path.exists(_lib.LIB_PATH):
+    pytest.skip("libw4a16.so not built", allow_module_level=True)
+
+L = _lib.load()
+NULL = ctypes.c_void_p(0)
+FAKE = ctypes.c_void_p(0x10000)        # 16-byte aligned, never dereferenced
+ODD = ctypes.c_void_p(0x10008)         # misaligned
+INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 1, 2, 3, 5
+
+
+def call(x=FAKE, stride=64, wq=FAKE, ws=FAKE, bias=NULL, act=0, out=FAKE, M=64, F=64, K=64, dtype=1, space=FAKE,
+         nbytes=1 << 20):
+    return L.w8a8_gated(x, stride, wq, ws, bias, act, out, M, F, K, dtype, space, nbytes, NULL)
+
+
+def test_refusals():
+    for bad in (dict(M=0), dict(F=0), dict(F=-8), dict(F=60), dict(K=40), dict(stride=60), dict(stride=48),
+                dict(dtype=2), dict(act=-1), dict(act=3), dict(x=NULL), dict(wq=NULL), dict(ws=NULL), dict(out=NULL)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(x=ODD), dict(ws=ODD), dict(bias=ODD), dict(out=ODD), dict(space=ODD)):
+        assert call(**bad) == MISALIGNED, bad
+    for bad in (dict(F=(1 << 23) + 8), dict(F=1 << 62), dict(M=(1 << 21) + 1), dict(M=1 << 20, F=1 << 16),
+                dict(K=(1 << 17) + 16, stride=(1 << 17) + 16)):
+        assert call(**bad) == UNSUPPORTED, bad
+
+
+def test_workspace():
+    need = L.w8a8_gated_workspace_bytes(64, 64, 64)
+    assert need == 64 * 64 + 256 == L.w8a8_workspace_bytes(64, 128, 64, 1)       # codes and scales
+    assert call(nbytes=need - 1) == WORKSPACE and call(space=NULL, nbytes=0) == WORKSPACE
+    assert L.w8a8_gated_workspace_bytes(4, 2048, 4096) == 0                       # quantized inside
+    assert L.w8a8_gated_workspace_bytes(1, 131064, 16384) == 0
+    assert L.w8a8_gated_workspace_bytes(1, 131072, 16384) > 0                     # w is 4 GB
+    for bad in ((0, 64, 64), (1, 60, 64), (1, 64, 40), (1, 0, 64), (1, 1 << 62, 64)):
+        assert L.w8a8_gated_workspace_bytes(*bad) == -1, bad
+
+
+def test_oracle():
+    xq, wq = np.array([[1, 2]]), np.array([[3, 0], [1, -1], [2, 2], [0, 1]])
+    for act, f in (("silu", lambda g: g / (1 + math.exp(-g))),
+                   ("gelu", lambda g: g / 2 * (1 + math.erf(g / math.sqrt(2)))),
+                   ("gelu_tanh", lambda g: g / 2 * (1 + math.tanh(math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3))))):
+        y = w8a8.gated(xq, [0.5], wq, [1.0, 1.0, 1.0, 2.0], [0.5, 0.0, 0.0, -1.0], act)[0]
+        assert np.allclose(y, [[f(2.0) * 3.0, f(-0.5) * 1.0]], rtol=1e-14)
