@@ -289,11 +289,12 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / TL::WN, wn = wave % TL::WN;
   const int KT = (K + 127) >> 7;
-  // (gated: rw the gate's rows, ru the up projection's)
+  // (gated: the waves being even in number, a wave's blocks are all of the gate's
+  // rows or all of the up projection's)
   constexpr int HALVES = ACT ? 2 : 1;
-  const uint32_t w_bytes = (uint32_t)min(TL::BN, N - col0) / HALVES * (uint32_t)K;
-  const rsrc_t rw = make_rsrc(wq + (size_t)(col0 / HALVES) * K, w_bytes);
-  const rsrc_t ru = ACT ? make_rsrc(wq + (size_t)(gate.F + col0 / HALVES) * K, w_bytes) : rw;
+  static_assert(TL::WAVES % 2 == 0, "blocks of w in turn");
+  const rsrc_t rw = make_rsrc(wq + (size_t)((ACT && (wave & 1) ? gate.F : 0) + col0 / HALVES) * K,
+                              (uint32_t)min(TL::BN, N - col0) / HALVES * (uint32_t)K);
   const rsrc_t rx = make_rsrc(xq + (size_t)row0 * K, (uint32_t)min(TL::BM, M - row0) * (uint32_t)K);
 
   // load i of this wave fills the LDS block WAVES i + wave (8 rows); blocks
@@ -307,8 +308,7 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     const uint32_t from = ACT && is_w ? 8u * (uint32_t)(blk >> 1) + (uint32_t)lrow : row;
     const uint32_t off =
         128 * t + 16 * (int)chunk < K ? from * (uint32_t)K + 16u * chunk : kOutOfRange;
-    dma16(!is_w ? rx : ACT && (blk & 1) ? ru : rw, lds + (t % NS) * TL::STAGE + blk * 1024, off,
-          t * 128);
+    dma16(is_w ? rw : rx, lds + (t % NS) * TL::STAGE + blk * 1024, off, t * 128);
   };
 
   const int r = lane & 31, h = lane >> 5;
@@ -657,15 +657,12 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 // 8 values of up to kRows rows of 4096 (a longer row counts as several).
 constexpr int kRows = 4;
 
-//
-// Gated, w is one buffer (less than 4 GB): 8 of the 16 rows of a product are the
-// gate's, 8 the up projection's.
-template <int DT, int MB, int NT, bool FUSED, int AHEAD, int ACT>
+template <int DT, int MB, int NT, bool FUSED, int AHEAD>
 __global__ void __launch_bounds__(512)
 w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __restrict__ sx,
                    const int8_t* __restrict__ wq, const float* __restrict__ sw,
                    const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
-                   int K, Gate gate) {
+                   int K) {
   constexpr int kSum = 8 * NT * MB * 1024, kCodes = FUSED ? kRows * 4096 + 16 * 16 : 0;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kSum > kCodes ? kSum : kCodes];
   __shared__ uint32_t mags[FUSED ? kRows : 1][8];
@@ -675,11 +672,8 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
   const int r = lane & 15, g = lane >> 4;
   const int col0 = (int)blockIdx.x * 16 * NT;
   const int KT = (K + 127) >> 7;
-  constexpr int HALVES = ACT ? 2 : 1;
-  const rsrc_t rw = ACT ? make_rsrc(wq, (uint32_t)N * (uint32_t)K)
-                        : make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(16 * NT, N - col0) * (uint32_t)K);
-  const uint32_t lane_row = ACT ? (uint32_t)(col0 / 2 + (r & 7) + (r & 8 ? gate.F : 0)) : (uint32_t)r;
-  const uint32_t lane_off = lane_row * (uint32_t)K + 16u * g;
+  const rsrc_t rw = make_rsrc(wq + (size_t)col0 * K, (uint32_t)min(16 * NT, N - col0) * (uint32_t)K);
+  const uint32_t lane_off = (uint32_t)r * (uint32_t)K + 16u * g;
   auto load_w = [&](int s, i32x4_t (&w)[2][NT]) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -687,8 +681,8 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
       for (int e = 0; e < 2; ++e)
         w[e][i] = __builtin_bit_cast(
             i32x4_t, bld128(rw,
-                            128 * s + 64 * e + 16 * g < K && (!ACT || col0 + 16 * i < N)
-                                ? lane_off + (uint32_t)(16 / HALVES * i) * (uint32_t)K + 64 * e
+                            128 * s + 64 * e + 16 * g < K
+                                ? lane_off + (uint32_t)(16 * i) * (uint32_t)K + 64 * e
                                 : kOutOfRange,
                             s * 128));
   };
@@ -788,35 +782,195 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
 #pragma unroll
     for (int j = 0; j < MB; ++j) part[((wave * NT + i) * MB + j) * 64 + r * 4 + g] = acc[i][j];
   __syncthreads();
-  auto sum_of = [&](int e) {
+  for (int e = tid; e < NT * MB * 64; e += 512) {
+    const int i = e / (64 * MB), j = e / 64 % MB, m = 16 * j + (e % 64) / 4, n = col0 + 16 * i + 4 * (e % 4);
     i32x4_t v = part[e];
 #pragma unroll
     for (int p = 1; p < 8; ++p) v += part[p * NT * MB * 64 + e];
-    return v;
-  };
-  // gated: entries 0 and 1 of a token's four are the gate's, 2 and 3 the up projection's
-  for (int at = tid; at < NT * MB * 64 / HALVES; at += 512) {
-    const int e = ACT ? (at >> 1) * 4 + (at & 1) : at;
-    const int i = e / (64 * MB), j = e / 64 % MB, m = 16 * j + (e % 64) / 4;
-    const int n = (col0 + 16 * i) / HALVES + 4 * (e % 4);
-    const i32x4_t v = sum_of(e);
-    if (m < M && n < N / HALVES) {
+    if (m < M && n < N) {
       const float4_t t = *(const float4_t*)(sw + n);
       float y[4];
 #pragma unroll
       for (int a = 0; a < 4; ++a)
         y[a] = result(v[a], scales[m], t[a], bias ? widen16<DT>(bias[n + a]) : 0.0f);
-      if constexpr (ACT != kNoGate) {
-        const i32x4_t vu = sum_of(e + 2);
-        float4_t tu, bu;
-        channels4<DT>(sw, bias, (int64_t)gate.F + n, tu, bu);
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-          y[a] = gated<ACT>(y[a], result(vu[a], scales[m], tu[a], bu[a]), gate);
-      }
-      *(u32x2_t*)(out + (size_t)m * (N / HALVES) + n) =
-          u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
+      *(u32x2_t*)(out + (size_t)m * N + n) = u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
     }
+  }
+}
+
+// The gated product of up to 16 tokens: the stream of w alone.  Workgroups of two
+// teams of 8 waves stay, one on a CU, and each team takes groups of 8 channels in
+// turn, 8 rows of the gate and 8 of the up projection in one product on
+// v_mfma_i32_16x16x64_i8; w is one buffer (less than 2 GB).
+//
+//  * Each workgroup has the tokens' codes in LDS, up to kCodes of them, brought
+//    there once while its first rows of w are on their way (all of the tokens' loads
+//    out first).  FUSED: from 16-bit rows of up to kFused values, which it quantizes
+//    for itself; more of them (16 x 4096 take every CU 12 us) are quantized by a
+//    launch before.
+//  * A team's waves take the steps of 128 codes of a group in turn, straight from
+//    memory into registers, AHEAD steps of a wave under way, across the groups'
+//    borders: no group waits for its first rows.
+//  * No wave waits for the others of its team: each leaves its sums of a group in
+//    LDS and counts itself, and the last one to arrive joins them.  There are two
+//    places in turn, and before a wave writes into one it sees (without a wait,
+//    unless it is two groups ahead) that the group before there has been joined;
+//    whoever joins that one waits for nobody, so the wait ends.
+constexpr int kCodes = 15 * 8192, kFused = 16384;
+
+template <int DT, int ACT, bool FUSED>
+__global__ void __launch_bounds__(1024)
+w8a8_gated_stream_kernel(const void* __restrict__ x, int64_t x_stride,
+                         const float* __restrict__ sx, const int8_t* __restrict__ wq, const float* __restrict__ sw,
+                         const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M,
+                         int K, Gate gate) {
+  constexpr int AHEAD = 4;
+  __shared__ __attribute__((aligned(16))) uint8_t codes[kCodes + 16 * 16];
+  __shared__ __attribute__((aligned(16))) i32x4_t part[2][2][8][64];
+  __shared__ uint32_t arrived[2][2], joined[2][2];  // waves; groups, 1 more than the last
+  __shared__ uint32_t mags[16];
+  __shared__ float scales[16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 7;
+  const int team = __builtin_amdgcn_readfirstlane(tid >> 9);
+  const int r = lane & 15, g = lane >> 4;
+  const int groups = gate.F >> 3, KT = (K + 127) >> 7;
+  const int first = (int)(blockIdx.x + gridDim.x * team), every = 2 * (int)gridDim.x;
+  // steps of a wave in a group, whole turns of its loads under way
+  const int steps = (int)ceil_div(KT, 8 * AHEAD) * AHEAD;
+
+  // ---- w: the next step that is loaded
+  const rsrc_t rw = make_rsrc(wq, (uint32_t)(2 * gate.F) * (uint32_t)K);
+  int lgroup = first, lk = 128 * wave;
+  uint32_t loff = (uint32_t)(lgroup * 8 + (r & 7) + (r & 8 ? gate.F : 0)) * (uint32_t)K + 16u * g;
+  i32x4_t w[AHEAD][2];
+  auto load = [&](int u) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      w[u][e] = __builtin_bit_cast(
+          i32x4_t, bld128(rw, lgroup < groups && lk + 64 * e + 16 * g < K ? loff + 64 * e : kOutOfRange, lk));
+    lk += 1024;
+    if (lk >= 1024 * steps) {
+      lk = 128 * wave;
+      lgroup += every;
+      loff += (uint32_t)every * 8u * (uint32_t)K;
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < AHEAD; ++u) load(u);
+
+  // ---- tokens: 16 bytes at a time, EACH values, unit i * 1024 + tid.  (its row: at
+  // is below 2^13, so (at + 1/2) / per is further from an integer than fp32's
+  // rounding moves it)
+  constexpr int EACH = FUSED ? 8 : 16, HOLD = (FUSED ? kFused : kCodes) / EACH / 1024 + !FUSED;
+  const int per = K / EACH, units = M * per, pitch = K + 16;
+  const float rows_per_unit = 1.0f / (float)per;
+  auto row_of = [&](int at) { return (int)(((float)at + 0.5f) * rows_per_unit); };
+  u32x4_t raw[HOLD];
+#pragma unroll
+  for (int i = 0; i < HOLD; ++i) {
+    const int at = i * 1024 + tid, m = row_of(at);
+    raw[i] = u32x4_t{0, 0, 0, 0};
+    if (at < units) {
+      if constexpr (FUSED)
+        raw[i] = *(const u32x4_t*)((const uint16_t*)x + m * x_stride + (at - m * per) * EACH);
+      else
+        raw[i] = *(const u32x4_t*)((const int8_t*)x + at * EACH);
+    }
+  }
+  if (tid < 4) arrived[tid >> 1][tid & 1] = joined[tid >> 1][tid & 1] = 0;
+  if constexpr (FUSED) {
+    if (tid < 16) mags[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      const int at = i * 1024 + tid, m = row_of(at);
+      if (i * 1024 >= units) break;
+      uint32_t mag = 0;
+      float f[8];
+      widen8<DT>(raw[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mag = max(mag, mag_bits(f[j]));
+      if (__all(m == __builtin_amdgcn_readfirstlane(m))) {
+        mag = lanes_max<64>(mag);
+        if (lane == 0 && at < units) atomicMax(mags + m, mag);
+      } else if (at < units) {
+        atomicMax(mags + m, mag);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      const int at = i * 1024 + tid, m = row_of(at), k = (at - m * per) * 8;
+      if (at >= units) break;
+      float s = scale_of(mags[m]), f[8];
+      if (s == 0.0f) s = 1.0f;
+      widen8<DT>(raw[i], f);
+      *(u32x2_t*)(codes + m * pitch + k) = codes8(f, Codes8(s));
+      if (k == 0) scales[m] = s;
+    }
+  } else {
+    if (tid < M) scales[tid] = sx[tid];
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      const int at = i * 1024 + tid, m = row_of(at);
+      if (at < units) *(u32x4_t*)(codes + m * pitch + (at - m * per) * EACH) = raw[i];
+    }
+  }
+  __syncthreads();
+
+  // ---- groups.  (tokens past the last repeat it; their results are not written)
+  const uint8_t* row = codes + min(r, M - 1) * pitch;
+  for (int turn = 0, group = first; group < groups; ++turn, group += every) {
+    i32x4_t acc = {0, 0, 0, 0};
+    for (int j = 0; j < steps; j += AHEAD) {
+      const int k = 1024 * j + 128 * wave + 16 * g;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+              w[u][e], *(const i32x4_t*)(row + min(k + 1024 * u + 64 * e, K - 16)), acc, 0, 0, 0);
+        load(u);
+      }
+    }
+    // ---- join: lane holds rows 4 g .. 4 g + 3 of the product, token r
+    const int place = turn & 1;
+    if (turn >= 2)
+      while (__hip_atomic_load(&joined[team][place], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) <
+             (uint32_t)turn - 1)
+        __builtin_amdgcn_s_sleep(1);
+    asm volatile("" ::: "memory");
+    part[team][place][wave][r * 4 + g] = acc;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    uint32_t count = 0;
+    if (lane == 0)
+      count = __hip_atomic_fetch_add(&arrived[team][place], 1u, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_WORKGROUP);
+    count = __builtin_amdgcn_readfirstlane(count);
+    asm volatile("" ::: "memory");
+    if (count != 8u * (turn >> 1) + 7u) continue;
+    i32x4_t v = part[team][place][0][lane];
+#pragma unroll
+    for (int p = 1; p < 8; ++p) v += part[team][place][p][lane];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (lane == 0)
+      __hip_atomic_store(&joined[team][place], (uint32_t)turn + 1, __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_WORKGROUP);
+    // lane: token lane / 4, of the gate channels 4 (lane & 1) .., of the up
+    // projection where lane & 2
+    const int m = lane >> 2, n = group * 8 + 4 * (lane & 1);
+    float4_t t, b;
+    channels4<DT>(sw, bias, (int64_t)n + (lane & 2 ? gate.F : 0), t, b);
+    float y[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const float own = result(v[a], scales[min(m, M - 1)], t[a], b[a]);
+      y[a] = gated<ACT>(own, __shfl_xor(own, 2, 64), gate);
+    }
+    if (m < M && !(lane & 2))
+      *(u32x2_t*)(out + (size_t)m * gate.F + n) =
+          u32x2_t{pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3])};
   }
 }
 
@@ -846,16 +1000,15 @@ void launch_tile(const Args& a, hipStream_t st) {
                a.gate);
 }
 
-template <int DT, int MB, int NT, bool FUSED, int ACT>
+template <int DT, int MB, int NT, bool FUSED>
 void launch_stream(const Args& a, hipStream_t st) {
   // rows of w under way per wave: where there is work before they are used,
   // 4 steps in all (1 x 4096 x 4096: 9.1 us with one step, 8.0 with four);
   // otherwise one, whose few registers leave room for a second workgroup
   // (16 x 4096 x 11008: 12.5 us, 13.4 with four; 8 x 5120 x 16384: 28, 30.2)
   constexpr int AHEAD = FUSED ? 4 / NT : 1;
-  launch_timed(w8a8_stream_kernel<DT, MB, NT, FUSED, AHEAD, ACT>,
-               dim3((unsigned)ceil_div(a.N, 16 * NT)), dim3(512), 0, st, a.x, a.x_stride, a.sx, a.wq,
-               a.sw, a.bias, a.out, a.M, a.N, a.K, a.gate);
+  launch_timed(w8a8_stream_kernel<DT, MB, NT, FUSED, AHEAD>, dim3((unsigned)ceil_div(a.N, 16 * NT)),
+               dim3(512), 0, st, a.x, a.x_stride, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K);
 }
 
 // Whether w8a8_linear quantizes inside the product.
@@ -892,10 +1045,10 @@ hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
   const int64_t t256 = ceil_div(a.M, 256) * ceil_div(a.N, 256);
   const int64_t c64 = 3 * std::max<int64_t>(t64, 256), c128 = 6 * 256 * ceil_div(t128, 256),
                 c256 = 16 * 256 * ceil_div(t256, 256);
-  if (a.M <= 64 && ceil_div(a.M, 16) * a.N < 12288) {
-    if (a.M > 32) launch_stream<DT, 4, 1, false, ACT>(a, st);
-    else if (a.M > 16) launch_stream<DT, 2, 1, false, ACT>(a, st);
-    else launch_stream<DT, 1, 1, false, ACT>(a, st);
+  if (!ACT && a.M <= 64 && ceil_div(a.M, 16) * a.N < 12288) {
+    if (a.M > 32) launch_stream<DT, 4, 1, false>(a, st);
+    else if (a.M > 16) launch_stream<DT, 2, 1, false>(a, st);
+    else launch_stream<DT, 1, 1, false>(a, st);
   } else if (c64 <= c128 && c64 <= c256) {
     launch_tile<DT, T64, ACT>(a, st);
   } else if (c128 <= c256) {
@@ -915,11 +1068,11 @@ hipError_t launch_gemm(const int8_t* xq, const float* sx, const int8_t* wq, cons
 
 // Channels per workgroup: 64 where that leaves two workgroups for each of 256
 // CUs, else 32, else 16 (each reads and quantizes the tokens for itself).
-template <int DT, int ACT>
+template <int DT>
 void launch_fused_dt(const Args& a, hipStream_t st) {
-  if (a.N >= 512 * 64) launch_stream<DT, 1, 4, true, ACT>(a, st);
-  else if (a.N >= 512 * 32) launch_stream<DT, 1, 2, true, ACT>(a, st);
-  else launch_stream<DT, 1, 1, true, ACT>(a, st);
+  if (a.N >= 512 * 64) launch_stream<DT, 1, 4, true>(a, st);
+  else if (a.N >= 512 * 32) launch_stream<DT, 1, 2, true>(a, st);
+  else launch_stream<DT, 1, 1, true>(a, st);
 }
 
 hipError_t launch_fused(const void* x, int64_t x_stride, const int8_t* wq, const float* sw,
@@ -927,24 +1080,36 @@ hipError_t launch_fused(const void* x, int64_t x_stride, const int8_t* wq, const
                         hipStream_t st) {
   const Args a = {x, x_stride, nullptr, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M,
                   (int)N, (int)K, {}};
-  (dtype == DT_F16 ? launch_fused_dt<DT_F16, kNoGate> : launch_fused_dt<DT_BF16, kNoGate>)(a, st);
+  (dtype == DT_F16 ? launch_fused_dt<DT_F16> : launch_fused_dt<DT_BF16>)(a, st);
   return hipGetLastError();
 }
 
-// Whether w8a8_gated quantizes inside the product: where w8a8_linear does and w
-// is one buffer.
-bool fused_gated(int64_t M, int64_t F, int64_t K) {
-  return fused(M, K) && 2 * F * K < ((int64_t)1 << 32);
+// Whether w8a8_gated takes the kernel for few tokens, and whether that quantizes.
+bool few_gated(int64_t M, int64_t F, int64_t K) {
+  return M <= 16 && M * K <= kCodes && 2 * F * K < ((int64_t)1 << 31);
+}
+bool fused_gated(int64_t M, int64_t F, int64_t K) { return few_gated(M, F, K) && M * K <= kFused; }
+
+template <int DT, int ACT, bool FUSED>
+void launch_gated_stream(const Args& a, hipStream_t st) {
+  launch_timed(w8a8_gated_stream_kernel<DT, ACT, FUSED>,
+               dim3((unsigned)std::min(a.gate.F >> 3, 256)), dim3(1024), 0, st, a.x, a.x_stride, a.sx,
+               a.wq, a.sw, a.bias, a.out, a.M, a.K, a.gate);
+}
+template <int DT, int ACT>
+hipError_t launch_gated_dt(const Args& a, hipStream_t st) {
+  if (!a.sx) launch_gated_stream<DT, ACT, true>(a, st);
+  else if (few_gated(a.M, a.gate.F, a.K)) launch_gated_stream<DT, ACT, false>(a, st);
+  else return launch_gemm_dt<DT, ACT>(a, st);
+  return hipGetLastError();
 }
 
 // A gated call on 16-bit rows (sx null) or on codes.
-template <int DT>
-hipError_t launch_gated(const Args& a, int act, hipStream_t st) {
-  if (a.sx == nullptr) {
-    (act == W4A16_GELU ? launch_fused_dt<DT, kErf> : launch_fused_dt<DT, kSigmoid>)(a, st);
-    return hipGetLastError();
-  }
-  return (act == W4A16_GELU ? launch_gemm_dt<DT, kErf> : launch_gemm_dt<DT, kSigmoid>)(a, st);
+hipError_t launch_gated(const Args& a, int act, int dtype, hipStream_t st) {
+  if (act == W4A16_GELU)
+    return (dtype == DT_F16 ? launch_gated_dt<DT_F16, kErf> : launch_gated_dt<DT_BF16, kErf>)(a, st);
+  return (dtype == DT_F16 ? launch_gated_dt<DT_F16, kSigmoid>
+                          : launch_gated_dt<DT_BF16, kSigmoid>)(a, st);
 }
 
 // --------------------------------------------------------------- checking ---
@@ -1055,7 +1220,7 @@ int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w
       a.x = xq;
       a.sx = sx;
     }
-    return hip_status((dtype == DT_F16 ? launch_gated<DT_F16> : launch_gated<DT_BF16>)(a, act, st));
+    return hip_status(launch_gated(a, act, dtype, st));
   });
 }
 

@@ -41,9 +41,11 @@ def test_workspace():
     need = L.w8a8_gated_workspace_bytes(64, 64, 64)
     assert need == 64 * 64 + 256 == L.w8a8_workspace_bytes(64, 128, 64, 1)       # codes and scales
     assert call(nbytes=need - 1) == WORKSPACE and call(space=NULL, nbytes=0) == WORKSPACE
-    assert L.w8a8_gated_workspace_bytes(4, 2048, 4096) == 0                       # quantized inside
-    assert L.w8a8_gated_workspace_bytes(1, 131064, 16384) == 0
-    assert L.w8a8_gated_workspace_bytes(1, 131072, 16384) > 0                     # w is 4 GB
+    # quantized inside: up to 16 rows of 16384 values in all, w below 2 GB
+    for M, F, K in ((4, 2048, 4096), (16, 4096, 1024), (1, 65528, 16384)):
+        assert L.w8a8_gated_workspace_bytes(M, F, K) == 0, (M, F, K)
+    for M, F, K in ((17, 2048, 64), (16, 4096, 1040), (1, 8, 16400), (1, 65536, 16384)):
+        assert L.w8a8_gated_workspace_bytes(M, F, K) >= M * K + 4 * M, (M, F, K)
     for bad in ((0, 64, 64), (1, 60, 64), (1, 64, 40), (1, 0, 64), (1, 1 << 62, 64)):
         assert L.w8a8_gated_workspace_bytes(*bad) == -1, bad
 

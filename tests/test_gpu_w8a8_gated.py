@@ -33,10 +33,11 @@ def check(y, x, wq, ws, b, act, dtype):
 
 
 SHAPES = [  # M, F, K
-    (1, 8, 16), (1, 2048, 4096), (2, 24, 48), (4, 1000, 1040), (1, 8200, 512), (2, 16392, 256),  # rows quantized inside
-    (3, 40, 4112), (7, 264, 4112), (16, 1000, 2064), (5, 5504, 5136),                            # w streamed
-    (17, 72, 5136), (31, 2048, 512), (33, 136, 80), (64, 512, 4096),
-    (16, 8192, 640), (100, 640, 1104), (129, 264, 5120), (255, 520, 1008),                       # 64 x 64 tiles
+    (1, 8, 16), (1, 2048, 4096), (2, 24, 48), (4, 1000, 1040), (1, 8200, 512), (2, 16392, 256),  # w streamed
+    (3, 40, 4112), (7, 264, 4112), (16, 1000, 2064), (5, 5504, 5136), (16, 8192, 640), (13, 520, 16),
+    (1, 264, 122880), (16, 24, 7680),                                                            # all of LDS
+    (17, 72, 5136), (31, 2048, 512), (33, 136, 80), (64, 512, 4096), (16, 264, 7696), (1, 40, 122896),
+    (100, 640, 1104), (129, 264, 5120), (255, 520, 1008),                                        # 64 x 64 tiles
     (333, 1792, 1280), (1000, 1016, 688), (512, 2568, 512),                                      # 128 x 128
     (2049, 2312, 320), (2304, 2304, 16), (8192, 2304, 144),                                      # 256 x 256
 ]
@@ -166,4 +167,4 @@ def test_refusals():
     with pytest.raises(TypeError):
         w4.w8a8_gated(x.cpu(), wq, ws)
     with pytest.raises(w4.W4A16Error, match="status 5"):
-        w4.w8a8_gated(x, wq, ws, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        w4.w8a8_gated(x.repeat(4, 1), wq, ws, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
