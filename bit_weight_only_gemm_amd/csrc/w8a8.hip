@@ -798,9 +798,9 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
   }
 }
 
-// The gated product of up to 16 tokens: the stream of w alone.  Workgroups of two
-// teams of 8 waves stay, one on a CU, and each team takes groups of 8 channels in
-// turn, 8 rows of the gate and 8 of the up projection in one product on
+// The gated product of up to 16 tokens: the stream of w alone.  Workgroups of 16
+// waves, teams of tw = 2, 4 or 8, stay, one on a CU, and each team takes groups of 8
+// channels in turn, 8 rows of the gate and 8 of the up projection in one product on
 // v_mfma_i32_16x16x64_i8; w is one buffer (less than 2 GB).
 //
 //  * Each workgroup has the tokens' codes in LDS, up to kCodes of them, brought
@@ -816,28 +816,28 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
 //    places in turn, and before a wave writes into one it sees (without a wait,
 //    unless it is two groups ahead) that the group before there has been joined;
 //    whoever joins that one waits for nobody, so the wait ends.
-constexpr int kCodes = 15 * 8192, kFused = 16384;
+constexpr int kCodes = 15 * 8192, kFused = 16384, kAhead = 4;
 
 template <int DT, int ACT, bool FUSED>
 __global__ void __launch_bounds__(1024)
 w8a8_gated_stream_kernel(const void* __restrict__ x, int64_t x_stride,
                          const float* __restrict__ sx, const int8_t* __restrict__ wq, const float* __restrict__ sw,
                          const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M,
-                         int K, Gate gate) {
-  constexpr int AHEAD = 4;
+                         int K, int tw, Gate gate) {
+  constexpr int AHEAD = kAhead;
   __shared__ __attribute__((aligned(16))) uint8_t codes[kCodes + 16 * 16];
-  __shared__ __attribute__((aligned(16))) i32x4_t part[2][2][8][64];
-  __shared__ uint32_t arrived[2][2], joined[2][2];  // waves; groups, 1 more than the last
+  __shared__ __attribute__((aligned(16))) i32x4_t part[2][16][64];
+  __shared__ uint32_t arrived[2][8], joined[2][8];  // waves; groups, 1 more than the last
   __shared__ uint32_t mags[16];
   __shared__ float scales[16];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 7;
-  const int team = __builtin_amdgcn_readfirstlane(tid >> 9);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & (tw - 1);
+  const int wave0 = __builtin_amdgcn_readfirstlane(tid >> 6) - wave, team = wave0 / tw;
   const int r = lane & 15, g = lane >> 4;
   const int groups = gate.F >> 3, KT = (K + 127) >> 7;
-  const int first = (int)(blockIdx.x + gridDim.x * team), every = 2 * (int)gridDim.x;
+  const int first = (int)(blockIdx.x + gridDim.x * team), every = 16 / tw * (int)gridDim.x;
   // steps of a wave in a group, whole turns of its loads under way
-  const int steps = (int)ceil_div(KT, 8 * AHEAD) * AHEAD;
+  const int steps = ((KT - 1) / (tw * AHEAD) + 1) * AHEAD;
 
   // ---- w: the next step that is loaded
   const rsrc_t rw = make_rsrc(wq, (uint32_t)(2 * gate.F) * (uint32_t)K);
@@ -849,8 +849,8 @@ w8a8_gated_stream_kernel(const void* __restrict__ x, int64_t x_stride,
     for (int e = 0; e < 2; ++e)
       w[u][e] = __builtin_bit_cast(
           i32x4_t, bld128(rw, lgroup < groups && lk + 64 * e + 16 * g < K ? loff + 64 * e : kOutOfRange, lk));
-    lk += 1024;
-    if (lk >= 1024 * steps) {
+    lk += 128 * tw;
+    if (lk >= 128 * tw * steps) {
       lk = 128 * wave;
       lgroup += every;
       loff += (uint32_t)every * 8u * (uint32_t)K;
@@ -878,7 +878,7 @@ w8a8_gated_stream_kernel(const void* __restrict__ x, int64_t x_stride,
         raw[i] = *(const u32x4_t*)((const int8_t*)x + at * EACH);
     }
   }
-  if (tid < 4) arrived[tid >> 1][tid & 1] = joined[tid >> 1][tid & 1] = 0;
+  if (tid < 16) arrived[tid >> 3][tid & 7] = joined[tid >> 3][tid & 7] = 0;
   if constexpr (FUSED) {
     if (tid < 16) mags[tid] = 0;
     __syncthreads();
@@ -924,38 +924,37 @@ w8a8_gated_stream_kernel(const void* __restrict__ x, int64_t x_stride,
   for (int turn = 0, group = first; group < groups; ++turn, group += every) {
     i32x4_t acc = {0, 0, 0, 0};
     for (int j = 0; j < steps; j += AHEAD) {
-      const int k = 1024 * j + 128 * wave + 16 * g;
+      const int k = 128 * tw * j + 128 * wave + 16 * g;
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-              w[u][e], *(const i32x4_t*)(row + min(k + 1024 * u + 64 * e, K - 16)), acc, 0, 0, 0);
+              w[u][e], *(const i32x4_t*)(row + min(k + 128 * tw * u + 64 * e, K - 16)), acc, 0, 0, 0);
         load(u);
       }
     }
     // ---- join: lane holds rows 4 g .. 4 g + 3 of the product, token r
     const int place = turn & 1;
     if (turn >= 2)
-      while (__hip_atomic_load(&joined[team][place], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) <
+      while (__hip_atomic_load(&joined[place][team], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) <
              (uint32_t)turn - 1)
         __builtin_amdgcn_s_sleep(1);
     asm volatile("" ::: "memory");
-    part[team][place][wave][r * 4 + g] = acc;
+    part[place][wave0 + wave][r * 4 + g] = acc;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     uint32_t count = 0;
     if (lane == 0)
-      count = __hip_atomic_fetch_add(&arrived[team][place], 1u, __ATOMIC_RELAXED,
+      count = __hip_atomic_fetch_add(&arrived[place][team], 1u, __ATOMIC_RELAXED,
                                      __HIP_MEMORY_SCOPE_WORKGROUP);
     count = __builtin_amdgcn_readfirstlane(count);
     asm volatile("" ::: "memory");
-    if (count != 8u * (turn >> 1) + 7u) continue;
-    i32x4_t v = part[team][place][0][lane];
-#pragma unroll
-    for (int p = 1; p < 8; ++p) v += part[team][place][p][lane];
+    if (count != (uint32_t)(tw * (turn >> 1) + tw - 1)) continue;
+    i32x4_t v = part[place][wave0][lane];
+    for (int p = 1; p < tw; ++p) v += part[place][wave0 + p][lane];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (lane == 0)
-      __hip_atomic_store(&joined[team][place], (uint32_t)turn + 1, __ATOMIC_RELAXED,
+      __hip_atomic_store(&joined[place][team], (uint32_t)turn + 1, __ATOMIC_RELAXED,
                          __HIP_MEMORY_SCOPE_WORKGROUP);
     // lane: token lane / 4, of the gate channels 4 (lane & 1) .., of the up
     // projection where lane & 2
@@ -1092,9 +1091,16 @@ bool fused_gated(int64_t M, int64_t F, int64_t K) { return few_gated(M, F, K) &&
 
 template <int DT, int ACT, bool FUSED>
 void launch_gated_stream(const Args& a, hipStream_t st) {
+  // waves of a team: as many as waste the fewest steps (a wave's are padded to
+  // turns of kAhead).  MI355X, 8 / 2 of them: 16 tokens by 27648 x 5120 (40 steps)
+  // 61.1 / 57.0 us, by 8192 x 4096 (32 steps, none wasted) 19.0 / 21.0
+  const int64_t KT = ceil_div(a.K, 128);
+  int tw = 2;
+  for (int n : {4, 8})
+    if (ceil_div(KT, n * kAhead) * n <= ceil_div(KT, tw * kAhead) * tw) tw = n;
   launch_timed(w8a8_gated_stream_kernel<DT, ACT, FUSED>,
                dim3((unsigned)std::min(a.gate.F >> 3, 256)), dim3(1024), 0, st, a.x, a.x_stride, a.sx,
-               a.wq, a.sw, a.bias, a.out, a.M, a.K, a.gate);
+               a.wq, a.sw, a.bias, a.out, a.M, a.K, tw, a.gate);
 }
 template <int DT, int ACT>
 hipError_t launch_gated_dt(const Args& a, hipStream_t st) {
