@@ -394,8 +394,8 @@ def _ws_cache(device, nbytes, stream=None, kept=None):
     return cur
 
 
-from .kv8 import (kv8_append, kv8_attention, kv8_attention_workspace_bytes,  # noqa: E402,F401
-                  kv8_cache, kv8_dequant)
+from .kv8 import (kv8_append, kv8_attention, kv8_attention_scored,  # noqa: E402,F401
+                  kv8_attention_workspace_bytes, kv8_cache, kv8_dequant)
 from .kv8_pages import (kv8_compact, kv8_copy_pages, kv8_fork, kv8_free,  # noqa: E402,F401
                         kv8_pages_workspace_bytes, kv8_refs, kv8_reserve)
 from .w8a8 import (w8a8_gated, w8a8_gated_workspace_bytes, w8a8_gemm,  # noqa: E402,F401

@@ -102,11 +102,68 @@ __device__ __forceinline__ float queries_f16(const u32x4_t (&w)[N], half8_t (&ou
 
 // Query rows of a (sequence, kv head): row i is token i / G, head i % G.  A
 // row tile is `rows` of them; it sees keys up to the largest limit of its rows.
-__device__ __forceinline__ int row_limit(const Kv8Seq& s, int causal, int j) {
-  return causal ? clamp_int(s.first + j + 1, 0, s.len) : s.len;
+// (prefix: keys below it are seen by every token that has a position)
+__device__ __forceinline__ int row_limit(const Kv8Seq& s, int causal, int j, int prefix = 0) {
+  const int p = s.first + j;
+  return causal ? clamp_int(p < 0 ? 0 : max(p + 1, prefix), 0, s.len) : s.len;
 }
-__device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, int rows, int G) {
-  return row_limit(s, causal, min((rt * rows + rows - 1) / G, s.n - 1));
+__device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, int rows, int G,
+                                          int prefix = 0) {
+  return row_limit(s, causal, min((rt * rows + rows - 1) / G, s.n - 1), prefix);
+}
+
+// What the scored form puts on the scores before the softmax, and which keys a
+// query sees:
+//   s <- cap tanh(s / cap) (cap > 0),  s <- s - slope[head] |position - l|,
+//   first[token] <= l < its limit, and below prefix[sequence] both ways.
+// Scores are in base 2 here (cap is times log2 e).  They are brought to their final
+// value before the maximum is taken, so that everything after it goes by them
+// with a factor of 1.
+struct Scoring {
+  float cap;
+  const float* slopes;    // [H] or null
+  const int32_t* first;   // [tokens] or null
+  const int32_t* prefix;  // [B] or null
+};
+
+// tanh(x) = 1 - 2 / (1 + exp(2 x)): one exponential and one reciprocal of 1 ulp and
+// three roundings, together 2^-20 off at most, which the cap multiplies: 5e-5 of a
+// probability under a cap of 50, where its rounding to fp16 is 5e-4.  Under larger
+// caps small scores are bent by the series instead (x - x^3 / 3 + 2 x^5 / 15 - 17 x^7
+// / 315, 2^-21 of itself off at 1 / 4), so that the error stays a part of the score.
+constexpr float kWideCap = 512.0f;
+__device__ __forceinline__ float bent(float s, float cap, float per_cap) {
+  const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s * per_cap));
+  return __builtin_fmaf(-2.0f * cap, r, cap);
+}
+__device__ __forceinline__ float bent_wide(float s, float cap, float per_cap) {
+  const float x = s / cap, y = x * x;
+  float t = __builtin_fmaf(y, -17.0f / 315.0f, 2.0f / 15.0f);
+  t = __builtin_fmaf(y, __builtin_fmaf(y, t, -1.0f / 3.0f), 1.0f);
+  return fabsf(x) < 0.25f ? s * t : bent(s, cap, per_cap);
+}
+
+// The final scores of N tokens from t on, from products that are to be multiplied
+// by f.  back: the query's position less t.
+template <int N>
+__device__ __forceinline__ void scored(float (&s)[N], float f, const Scoring& sc, float slope,
+                                       float back) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] *= f;
+  if (sc.cap > 0.0f) {
+    const float per_cap = 2.0f * kLog2e / sc.cap;
+    if (sc.cap > kWideCap) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = bent_wide(s[i], sc.cap, per_cap);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = bent(s[i], sc.cap, per_cap);
+    }
+  }
+  if (sc.slopes) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __builtin_fmaf(-slope, fabsf(back - (float)i), s[i]);
+  }
 }
 
 // Units of a split: this sequence's in equal shares, none below the planned.
@@ -167,11 +224,11 @@ __device__ __forceinline__ float four_rows_max(float x) {
 // With 16 rows to a wave and not more, three waves share a SIMD and cover each
 // other's waits: 32 or 48 rows a wave read the codes less often, and took 27 us
 // against 21 for 24 sequences of 4001, 40 rows of 64 channels a kv head.
-template <int DT, int D>
+template <int DT, int D, bool SCORED>
 __global__ void __launch_bounds__(256)
 kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float scale, int causal,
                   uint16_t* __restrict__ out, int64_t out_stride, float* __restrict__ lse,
-                  Parts parts, int row_tiles, int splits, int units) {
+                  Parts parts, int row_tiles, int splits, int units, Scoring sc) {
   constexpr int DC = D / 64, DN = D / 16;
   __shared__ float joined[4][16][D + 4];
   __shared__ float stat[4][2][16];
@@ -189,16 +246,33 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const int G = c.H / c.Hkv;
   const Kv8Seq seq = kv8_seq(c, b);
   if (rt * 16 >= seq.n * G) return;
-  const int top = tile_limit(seq, causal, rt, 16, G);
-  const int nu = (top + kUnit - 1) / kUnit;
-  const int share = split_units(nu, splits, units);
-  const int u0 = split * share, u1 = min(u0 + share, nu);
-  if (split > 0 && u0 >= nu) return;
-
   const int ridx = rt * 16 + col;
   const bool rv = ridx < seq.n * G;
   const int tok = seq.tok + (rv ? ridx / G : 0), head = hk * G + (rv ? ridx % G : 0);
-  const int lim = rv ? row_limit(seq, causal, ridx / G) : 0;
+  const int prefix = SCORED && sc.prefix ? sc.prefix[b] : 0;
+  const int lim = rv ? row_limit(seq, causal, ridx / G, prefix) : 0;
+  // first key that this row sees, that some row and that every row does
+  int low = 0, low_min = 0, low_max = 0;
+  if (SCORED && sc.first) {
+    low = rv ? max(sc.first[tok], 0) : 0;
+    low_max = low;
+    low_min = rv ? low : INT32_MAX;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      low_max = max(low_max, __shfl_xor(low_max, o, 64));
+      low_min = min(low_min, __shfl_xor(low_min, o, 64));
+    }
+    low_max = __builtin_amdgcn_readfirstlane(low_max);
+    low_min = __builtin_amdgcn_readfirstlane(low_min);
+  }
+  const float slope = SCORED && sc.slopes ? sc.slopes[head] * kLog2e : 0.0f;
+
+  // units nu0 .. nu - 1, this split's u0 .. u1 - 1
+  const int top = tile_limit(seq, causal, rt, 16, G, prefix);
+  const int nu = (top + kUnit - 1) / kUnit, nu0 = min(low_min / kUnit, nu);
+  const int share = split_units(nu - nu0, splits, units);
+  const int u0 = nu0 + split * share, u1 = min(u0 + share, nu);
+  if (split > 0 && u0 >= nu) return;
 
   // ---- queries: channels 64 c + 16 g + 8 e .. + 7 of this lane's row
   half8_t qf[DC][2];
@@ -264,7 +338,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     turn_pages(u0 + wave + 4);
   }
   // keys that every row of the tile sees
-  const int lim_all = row_limit(seq, causal, rt * 16 / G);
+  const int lim_all = row_limit(seq, causal, rt * 16 / G, prefix);
   const bool whole = c.lgT >= 6;  // a unit lies in one page
   for (int u = u0 + wave; u < u1; u += 4) {
     const int t0 = u * kUnit;
@@ -282,19 +356,32 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     load_keys(u + 4);
     __builtin_amdgcn_sched_barrier(0);
     // past the sequence's end it may be no page of this sequence
-    const bool held = whole || t0 + 16 * g < seq.len;
+    // (scored: nor does the scale matter of tokens that no row sees)
+    const bool held = (whole || t0 + 16 * g < seq.len) &&
+                      (!SCORED || t0 + (whole ? 63 : 16 * g + 15) >= low_min);
     float f = held ? f_row * ks : 0.0f;
-    if (f == 0.0f) f = 1e-37f;  // a hidden key stays at -inf
+    if constexpr (SCORED) {
+      float t[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t[i] = s[i >> 2][i & 3];
+      scored(t, f, sc, slope, (float)(seq.first + ridx / G - t0 - 16 * g));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] = t[i];
+      f = 1.0f;
+    } else if (f == 0.0f) {
+      f = 1e-37f;  // a hidden key stays at -inf
+    }
     const float v_scale = held ? vs : 0.0f;
     const float vs_top = whole ? v_scale : four_rows_max(v_scale);
     // rows past the tile's last see what the others do; they are not written
-    const bool edge = t0 + kUnit > lim_all;
+    const bool edge = t0 + kUnit > lim_all || (SCORED && t0 < low_max);
+    auto hidden = [&](int l) { return l >= lim || (SCORED && l < low); };
     if (edge) {
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (t0 + 16 * g + 4 * a + i >= lim) s[a][i] = -INFINITY;
+          if (hidden(t0 + 16 * g + 4 * a + i)) s[a][i] = -INFINITY;
     }
     float mx = fmaxf(s[0][0], s[0][1]);
 #pragma unroll
@@ -342,7 +429,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (t0 + 16 * g + 4 * a + i >= lim) s[a][i] = 0.0f;
+          if (hidden(t0 + 16 * g + 4 * a + i)) s[a][i] = 0.0f;
     }
 #pragma unroll
     for (int a = 0; a < 4; ++a)
@@ -397,7 +484,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   }
   const int64_t tk = seq.tok + min(rr / G, seq.n - 1);
   const int hd = hk * G + rr % G;
-  const int mine = max(1, (nu + share - 1) / share);  // splits with a unit
+  const int mine = max(1, (nu - nu0 + share - 1) / share);  // splits with a unit
   if (mine > 1) {
     // ---- the last workgroup of the tile to arrive joins the splits, in order.
     // The partials go through the point where the GPU's caches meet (agent-scope
@@ -484,11 +571,11 @@ __device__ __forceinline__ int swizzle(int row) {
 template <int D>
 constexpr int kPromptWaves = D / 16;
 
-template <int DT, int D, bool WHOLE>
+template <int DT, int D, bool WHOLE, bool SCORED>
 __global__ void __launch_bounds__(64 * kPromptWaves<D>) __attribute__((amdgpu_waves_per_eu(1, 2)))
 kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float scale, int causal,
                   uint16_t* __restrict__ out, int64_t out_stride, float* __restrict__ lse,
-                  Parts parts, int row_tiles, int splits, int units) {
+                  Parts parts, int row_tiles, int splits, int units, Scoring sc) {
   // in iteration u the keys of u + 1 and the values of u are read, and both of
   // u + 2 written
   constexpr int NBK = 2, NBV = 3, W = kPromptWaves<D>;
@@ -513,18 +600,52 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const int G = c.H / c.Hkv;
   const Kv8Seq seq = kv8_seq(c, b);
   if (rt * ROWS >= seq.n * G) return;
-  const int top = tile_limit(seq, causal, rt, ROWS, G);
-  const int nu = (top + kUnit - 1) / kUnit;
-  const int share = split_units(nu, splits, units);
-  const int u0 = split * share, u1 = min(u0 + share, nu);
-  if (split > 0 && u0 >= nu) return;
-
   const int row0 = rt * ROWS + wave * 32, ridx = row0 + col;
   const bool rv = ridx < seq.n * G;
   const int tok = seq.tok + (rv ? ridx / G : 0), head = hk * G + (rv ? ridx % G : 0);
-  const int lim = rv ? row_limit(seq, causal, ridx / G) : 0;
+  const int prefix = SCORED && sc.prefix ? sc.prefix[b] : 0;
+  const int lim = rv ? row_limit(seq, causal, ridx / G, prefix) : 0;
   // keys that every row of this wave sees
-  const int lim_all = row0 + 31 < seq.n * G ? row_limit(seq, causal, row0 / G) : 0;
+  const int lim_all = row0 + 31 < seq.n * G ? row_limit(seq, causal, row0 / G, prefix) : 0;
+  // first key that this row sees, that some row of the workgroup and that every
+  // row of this wave does
+  int low = 0, low_min = 0, low_max = 0, low_wave = 0;
+  if constexpr (SCORED) {
+    __shared__ int lows[W];
+    if (sc.first) {
+      low = rv ? max(sc.first[tok], 0) : 0;
+      low_max = low;
+      low_min = rv ? low : INT32_MAX;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        low_max = max(low_max, __shfl_xor(low_max, o, 64));
+        low_min = min(low_min, __shfl_xor(low_min, o, 64));
+      }
+      low_max = __builtin_amdgcn_readfirstlane(low_max);
+      low_wave = __builtin_amdgcn_readfirstlane(low_min);
+      if (lane == 0) lows[wave] = low_min;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) low_min = min(low_min, lows[w]);
+      low_min = __builtin_amdgcn_readfirstlane(low_min);
+    }
+  }
+  const float slope = SCORED && sc.slopes ? sc.slopes[head] * kLog2e : 0.0f;
+
+  // units nu0 .. nu - 1, this split's u0 .. u1 - 1
+  const int top = tile_limit(seq, causal, rt, ROWS, G, prefix);
+  const int nu = (top + kUnit - 1) / kUnit, nu0 = min(low_min / kUnit, nu);
+  const int share = split_units(nu - nu0, splits, units);
+  const int u0 = nu0 + split * share, u1 = min(u0 + share, nu);
+  if (split > 0 && u0 >= nu) {
+    // (scored: the join does not know which splits have units)
+    if (SCORED && rv && h == 0) {
+      const int64_t at_p = ((int64_t)tok * c.H + head) * splits + split;
+      parts.ml[at_p * 2] = kNone;
+      parts.ml[at_p * 2 + 1] = 0.0f;
+    }
+    return;
+  }
 
   half8_t qf[Q_LDS ? 1 : KS];
   uint8_t* q_mine = lds + (NBK + NBV) * BUF + (wave * KS * 64 + lane) * 16;
@@ -642,10 +763,27 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     for (int a = 0; a < NSC; ++a) {
       asm volatile("" : "+v"(ks_next[a]), "+v"(vs_next[a]));
       // past the sequence's end it may be no page of this sequence
-      const bool held = WHOLE || t0 + 32 * a + 16 * h < seq.len;
+      // (scored: nor does the scale matter of tokens that no row of the wave sees)
+      const bool held = (WHOLE || t0 + 32 * a + 16 * h < seq.len) &&
+                        (!SCORED || t0 + (WHOLE ? 63 : 32 * a + 16 * h + 15) >= low_wave);
       f[a] = held ? f_row * ks_next[a] : 0.0f;
       vs[a] = held ? vs_next[a] : 0.0f;
-      if (f[a] == 0.0f) f[a] = 1e-37f;  // a hidden key stays at -inf
+      if (!SCORED && f[a] == 0.0f) f[a] = 1e-37f;  // a hidden key stays at -inf
+    }
+    auto hidden = [&](int l) { return l >= lim || (SCORED && l < low); };
+    if constexpr (SCORED) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        float t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] = s[a][i];
+        scored(t, f[WHOLE ? 0 : a], sc, slope,
+               (float)(seq.first + ridx / G - t0 - 32 * a - 16 * h));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[a][i] = t[i];
+      }
+#pragma unroll
+      for (int a = 0; a < NSC; ++a) f[a] = 1.0f;
     }
     vs_top = vs[0];
     if constexpr (!WHOLE) vs_top = both_halves_max(fmaxf(vs[0], vs[1]));
@@ -656,7 +794,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       if (EDGE) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (t0 + 32 * a + 16 * h + i >= lim) s[a][i] = -INFINITY;
+          if (hidden(t0 + 32 * a + 16 * h + i)) s[a][i] = -INFINITY;
       }
       float t = fmaxf(s[a][0], s[a][1]);
 #pragma unroll
@@ -720,7 +858,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
         const int a = x >> 4, i = x & 15, z = WHOLE ? 0 : a;
         float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], f[z], shift[z]));
         // exactly 0 where hidden, whatever the page's scales are
-        if (EDGE && t0 + 32 * a + 16 * h + i >= lim) p = 0.0f;
+        if (EDGE && hidden(t0 + 32 * a + 16 * h + i)) p = 0.0f;
         sum[z] += p;
         pf[a][i >> 3][i & 7] = (_Float16)p;
       }
@@ -781,13 +919,25 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     vb = vb == 2 ? 0 : vb + 1;
   };
   int u = u0;
-  for (; u + 1 < u1 && (u + 2) * kUnit <= lim_all; u += 2) {
-    turn(std::false_type{}, even, odd, u, 0);
-    turn(std::false_type{}, odd, even, u + 1, 1);
-  }
-  for (; u < u1; u += 2) {
-    turn(std::true_type{}, even, odd, u, 0);
-    if (u + 1 < u1) turn(std::true_type{}, odd, even, u + 1, 1);
+  if constexpr (SCORED) {
+    for (; u < u1; u += 2) {
+      if (u * kUnit >= low_max && u + 1 < u1 && (u + 2) * kUnit <= lim_all) {
+        turn(std::false_type{}, even, odd, u, 0);
+        turn(std::false_type{}, odd, even, u + 1, 1);
+      } else {
+        turn(std::true_type{}, even, odd, u, 0);
+        if (u + 1 < u1) turn(std::true_type{}, odd, even, u + 1, 1);
+      }
+    }
+  } else {
+    for (; u + 1 < u1 && (u + 2) * kUnit <= lim_all; u += 2) {
+      turn(std::false_type{}, even, odd, u, 0);
+      turn(std::false_type{}, odd, even, u + 1, 1);
+    }
+    for (; u < u1; u += 2) {
+      turn(std::true_type{}, even, odd, u, 0);
+      if (u + 1 < u1) turn(std::true_type{}, odd, even, u + 1, 1);
+    }
   }
   l += __shfl_xor(l, 32, 64);
 
@@ -825,7 +975,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
 
 // Joins the prompt kernel's splits of a row, in their order: one wave per
 // (token, head).
-template <int DT, int D>
+template <int DT, int D, bool SCORED>
 __global__ void __launch_bounds__(256)
 kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_stride,
                 float* __restrict__ lse, Parts parts, int splits, int units, int rows, int max_new) {
@@ -836,10 +986,14 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
   const int hd = (int)(i % c.H), j = (int)(i / c.H % max_new), b = (int)(i / c.H / max_new);
   const Kv8Seq seq = kv8_seq(c, b);
   if (j >= seq.n) return;
-  const int top = tile_limit(seq, causal, (j * G + hd % G) / rows, rows, G);
-  const int nu = (top + kUnit - 1) / kUnit;
-  const int share = split_units(nu, splits, units);
-  const int n = max((nu + share - 1) / share, 1);
+  // (scored: every split has left its sum, those without units a 0)
+  int n = splits;
+  if constexpr (!SCORED) {
+    const int top = tile_limit(seq, causal, (j * G + hd % G) / rows, rows, G);
+    const int nu = (top + kUnit - 1) / kUnit;
+    const int share = split_units(nu, splits, units);
+    n = max((nu + share - 1) / share, 1);
+  }
   const int64_t row = (int64_t)(seq.tok + j) * c.H + hd;
   float m = -INFINITY;
   for (int s = 0; s < n; ++s) m = fmaxf(m, parts.ml[(row * splits + s) * 2]);
@@ -849,6 +1003,7 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
   for (int s = 0; s < n; ++s) {
     const int64_t at = row * splits + s;
     const float w = __builtin_amdgcn_exp2f(parts.ml[at * 2] - base);
+    if (SCORED && parts.ml[at * 2 + 1] == 0.0f) continue;  // saw nothing
     l += w * parts.ml[at * 2 + 1];
 #pragma unroll
     for (int e = 0; e < E; ++e) r[e] += w * parts.o[at * D + lane * E + e];
@@ -901,10 +1056,10 @@ int64_t part_bytes(const Plan& p, int64_t tokens, int H, int D) {
   return kCounters * 4 + pad256(rows * D * 4) + pad256(rows * 8);
 }
 
-template <int DT, int D>
+template <int DT, int D, bool SCORED>
 hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t q_stride,
                             float scale, int causal, void* out, int64_t out_stride, float* lse,
-                            int64_t max_new, void* ws, hipStream_t st) {
+                            int64_t max_new, void* ws, const Scoring& sc, hipStream_t st) {
   const int64_t rows = (int64_t)c.tokens * c.H * p.splits;
   Parts parts = {(float*)((uint8_t*)ws + kCounters * 4), nullptr, (uint32_t*)ws};
   parts.ml = parts.o + pad256(rows * D * 4) / 4;
@@ -912,19 +1067,66 @@ hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t 
   auto go = [&](auto kernel, int64_t grid, int threads) {
     launch_timed(kernel, dim3((unsigned)grid), dim3(threads), 0, st, c, (const uint16_t*)q,
                  q_stride, scale, causal, (uint16_t*)out, out_stride, lse, parts, p.row_tiles,
-                 p.splits, p.units);
+                 p.splits, p.units, sc);
   };
   const int64_t grid = 8 * ceil_div(groups, 8) * p.row_tiles;
   const bool whole = (1 << c.lgT) >= kUnit;
-  if (p.waves == 0) go(kv8_decode_kernel<DT, D>, grid, 256);
-  else if (whole) go(kv8_prompt_kernel<DT, D, true>, grid, 64 * kPromptWaves<D>);
-  else go(kv8_prompt_kernel<DT, D, false>, grid, 64 * kPromptWaves<D>);
+  if (p.waves == 0) go(kv8_decode_kernel<DT, D, SCORED>, grid, 256);
+  else if (whole) go(kv8_prompt_kernel<DT, D, true, SCORED>, grid, 64 * kPromptWaves<D>);
+  else go(kv8_prompt_kernel<DT, D, false, SCORED>, grid, 64 * kPromptWaves<D>);
   if (p.waves && p.splits > 1)
-    hipLaunchKernelGGL((kv8_join_kernel<DT, D>),
+    hipLaunchKernelGGL((kv8_join_kernel<DT, D, SCORED>),
                        dim3((unsigned)ceil_div((int64_t)c.B * max_new * c.H, 4)), dim3(256), 0,
                        st, c, causal, (uint16_t*)out, out_stride, lse, parts, p.splits, p.units, p.rows,
                        (int)max_new);
   return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace w4a16
+
+namespace w4a16 {
+namespace {
+template <bool SCORED>
+int attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+              const float* k_scale, const float* v_scale, int64_t num_pages, int32_t page_size,
+              const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens,
+              const int32_t* cu_seqlens, float scale, int32_t causal, const Scoring& sc, void* out,
+              int64_t out_stride, float* lse, int64_t tokens, int64_t B, int64_t max_new,
+              int64_t max_len, int32_t H, int32_t Hkv, int32_t D, int32_t dtype, void* workspace,
+              int64_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    if (int s = validate_kv8(num_pages, page_size, max_pages, tokens, B, max_new, H, Hkv, D,
+                             cu_seqlens))
+      return s;
+    if (int s = validate_dtype(dtype)) return s;
+    if (max_len < 0 || max_len > max_pages * page_size) return W4A16_ERR_INVALID_ARG;
+    if (bad_stride(q_stride, (int64_t)H * D) || bad_stride(out_stride, (int64_t)H * D))
+      return W4A16_ERR_INVALID_ARG;
+    if (tokens == 0 || B == 0 || max_new == 0) return W4A16_OK;
+    if (int s = check_ptrs({q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out}))
+      return s;
+    for (const void* p : {(const void*)cu_seqlens, (const void*)lse, (const void*)workspace,
+                          (const void*)sc.slopes, (const void*)sc.first, (const void*)sc.prefix})
+      if (!aligned16(p)) return W4A16_ERR_MISALIGNED;
+    const Plan p = plan_attention(B, max_new, max_len, H, Hkv, D);
+    const int64_t need = part_bytes(p, tokens, H, D);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+    // (the join's grid is smaller: it runs where there are less than 512 row tiles)
+    if (too_large(8 * ceil_div(B * Hkv * p.splits, 8) * p.row_tiles, p.waves ? 64 * p.waves : 256))
+      return W4A16_ERR_UNSUPPORTED;
+    clear_pending_error();
+    const Kv8 c = {const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(v_cache),
+                   const_cast<float*>(k_scale), const_cast<float*>(v_scale), page_table, seq_lens,
+                   cu_seqlens, (int)num_pages, (int)max_pages, (int)B, (int)tokens, (int)max_new, H,
+                   Hkv, log2_page(page_size)};
+    auto* f = D == 64 ? (dtype == DT_F16 ? launch_attention<DT_F16, 64, SCORED>
+                                         : launch_attention<DT_BF16, 64, SCORED>)
+                      : (dtype == DT_F16 ? launch_attention<DT_F16, 128, SCORED>
+                                         : launch_attention<DT_BF16, 128, SCORED>);
+    return hip_status(f(c, p, q, q_stride, scale, causal, out, out_stride, lse, max_new, workspace,
+                        sc, (hipStream_t)stream));
+  });
 }
 
 }  // namespace
@@ -950,37 +1152,28 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
                   void* out, int64_t out_stride, float* lse, int64_t tokens, int64_t B,
                   int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
                   int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
-  return guarded([&]() -> int {
-    if (int s = validate_kv8(num_pages, page_size, max_pages, tokens, B, max_new, H, Hkv, D,
-                             cu_seqlens))
-      return s;
-    if (int s = validate_dtype(dtype)) return s;
-    if (max_len < 0 || max_len > max_pages * page_size) return W4A16_ERR_INVALID_ARG;
-    if (bad_stride(q_stride, (int64_t)H * D) || bad_stride(out_stride, (int64_t)H * D))
-      return W4A16_ERR_INVALID_ARG;
-    if (tokens == 0 || B == 0 || max_new == 0) return W4A16_OK;
-    if (int s = check_ptrs({q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out}))
-      return s;
-    for (const void* p : {(const void*)cu_seqlens, (const void*)lse, (const void*)workspace})
-      if (!aligned16(p)) return W4A16_ERR_MISALIGNED;
-    const Plan p = plan_attention(B, max_new, max_len, H, Hkv, D);
-    const int64_t need = part_bytes(p, tokens, H, D);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
-    // (the join's grid is smaller: it runs where there are less than 512 row tiles)
-    if (too_large(8 * ceil_div(B * Hkv * p.splits, 8) * p.row_tiles, p.waves ? 64 * p.waves : 256))
-      return W4A16_ERR_UNSUPPORTED;
-    clear_pending_error();
-    const Kv8 c = {const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(v_cache),
-                   const_cast<float*>(k_scale), const_cast<float*>(v_scale), page_table, seq_lens,
-                   cu_seqlens, (int)num_pages, (int)max_pages, (int)B, (int)tokens, (int)max_new, H,
-                   Hkv, log2_page(page_size)};
-    auto* f = D == 64 ? (dtype == DT_F16 ? launch_attention<DT_F16, 64>
-                                         : launch_attention<DT_BF16, 64>)
-                      : (dtype == DT_F16 ? launch_attention<DT_F16, 128>
-                                         : launch_attention<DT_BF16, 128>);
-    return hip_status(f(c, p, q, q_stride, scale, causal, out, out_stride, lse, max_new, workspace,
-                        (hipStream_t)stream));
-  });
+  return attention<false>(q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
+                          page_table, max_pages, seq_lens, cu_seqlens, scale, causal, Scoring{},
+                          out, out_stride, lse, tokens, B, max_new, max_len, H, Hkv, D, dtype,
+                          workspace, workspace_bytes, stream);
+}
+
+int kv8_attention_scored(const void* q, int64_t q_stride, const uint8_t* k_cache,
+                         const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                         int64_t num_pages, int32_t page_size, const int32_t* page_table,
+                         int64_t max_pages, const int32_t* seq_lens, const int32_t* cu_seqlens,
+                         float scale, int32_t causal, float softcap, const float* slopes,
+                         const int32_t* first, const int32_t* prefix, void* out,
+                         int64_t out_stride, float* lse, int64_t tokens, int64_t B,
+                         int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
+                         int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  // (beyond these the quotients of scores and cap leave fp32)
+  if (softcap != 0.0f && !(softcap >= 1e-3f && softcap <= 1e30f)) return W4A16_ERR_INVALID_ARG;
+  const Scoring sc = {softcap * kLog2e, slopes, first, prefix};
+  return attention<true>(q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
+                         page_table, max_pages, seq_lens, cu_seqlens, scale, causal, sc, out,
+                         out_stride, lse, tokens, B, max_new, max_len, H, Hkv, D, dtype, workspace,
+                         workspace_bytes, stream);
 }
 
 }  // extern "C"

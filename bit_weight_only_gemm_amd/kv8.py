@@ -6,7 +6,8 @@ that fills it and the attention that reads it (the ``kv8_*`` entry points of
     q = kv8_append(cache, k, v, page_table, seq_lens, q=q, cos=cos, sin=sin)
     o = kv8_attention(q, cache, page_table, seq_lens)
 
-page_table int32 [B, max_pages], seq_lens int32 [B] (the new tokens included)
+(kv8_attention_scored: with capped scores, a bias by distance, document and
+prefix masks.)  page_table int32 [B, max_pages], seq_lens int32 [B] (the new tokens included)
 and cu_seqlens int32 [B + 1] stay on the device; without cu_seqlens each
 sequence has one new token.  Rows of q, k and v are [tokens, heads, D] and may
 be slices of a fused projection.
@@ -18,7 +19,7 @@ import math
 
 import torch
 
-from . import _DT, _lib, _need, _stream
+from . import _DT, _here, _lib, _need, _stream
 from .w8a8 import _empty, _space
 
 
@@ -166,6 +167,35 @@ def kv8_attention(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
     kv8_attention_workspace_bytes, kept for these calls alone and zero before
     the first (one per stream is kept when not given): it holds counters, and
     one that another operator has written in leaves results unwritten."""
+    return _attention("kv8_attention", None, q, cache, page_table, seq_lens, cu_seqlens, max_new,
+                      max_len, scale, causal, out, lse, workspace, stream)
+
+
+def kv8_attention_scored(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
+                         max_len=None, scale=None, causal=True, softcap=0.0, slopes=None,
+                         first=None, prefix=None, out=None, lse=None, workspace=None, stream=None):
+    """kv8_attention of scores s = scale q . k that become softcap tanh(s /
+    softcap) (0 or None: as they are), less slopes[h] |distance| (fp32 [H]).
+    first (int32 [tokens]): the first position that each query sees, the start of
+    its document or of a window.  prefix (int32 [B]): with causal, positions below
+    it are seen by every query of the sequence.  A query that sees nothing gives 0.
+    The other arguments as for kv8_attention, its workspace among them."""
+    softcap = 0.0 if softcap is None else float(softcap)
+    extra = [softcap, None, None, None]
+    for i, (t, dtype, name, n) in enumerate(((slopes, torch.float32, "slopes", q.shape[1]),
+                                             (first, torch.int32, "first", q.shape[0]),
+                                             (prefix, torch.int32, "prefix", seq_lens.shape[0]))):
+        if t is not None:
+            _need(t, dtype, name, n)
+            extra[1 + i] = t.data_ptr()
+    _here(stream, q, cache["k"], page_table, seq_lens, cu_seqlens, slopes, first, prefix, out, lse,
+          workspace)
+    return _attention("kv8_attention_scored", extra, q, cache, page_table, seq_lens, cu_seqlens,
+                      max_new, max_len, scale, causal, out, lse, workspace, stream)
+
+
+def _attention(name, extra, q, cache, page_table, seq_lens, cu_seqlens, max_new, max_len, scale,
+               causal, out, lse, workspace, stream):
     pages, Hkv, T, D, arrays = _cache(cache)
     tokens, H, q_stride = _heads(q, None, "q", None, None, D)
     dtype = q.dtype
@@ -181,12 +211,12 @@ def kv8_attention(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
     L = _lib.lib()
     need = L.kv8_attention_workspace_bytes(tokens, B, max_new, max_len, H, Hkv, D)
     workspace, nbytes = _space(workspace, need, q.device, stream, _COUNTED)
-    status = L.kv8_attention(
+    status = getattr(L, name)(
         q.data_ptr(), q_stride, *arrays, pages, T, page_table.data_ptr(), width,
         seq_lens.data_ptr(), cu, 1.0 / math.sqrt(D) if scale is None else float(scale),
-        1 if causal else 0, out.data_ptr(), o_stride, None if lse is None else lse.data_ptr(),
+        1 if causal else 0, *(extra or ()), out.data_ptr(), o_stride, None if lse is None else lse.data_ptr(),
         tokens, B, max_new, max_len, H, Hkv, D, _DT[dtype],
         None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream))
     if status:
-        _lib.check(status, "kv8_attention")
+        _lib.check(status, name)
     return out

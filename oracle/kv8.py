@@ -91,3 +91,70 @@ def attention_bounds(out, mass, work, tokens_seen, D, dtype):
     d = ((D + 4) * 2.0 ** -23 * work + 2.0 ** -20)[..., None]
     rel = 2 * d + 2.0 ** -11 + (80 + tokens_seen / 64) * 2.0 ** -22 + tokens_seen * 2.0 ** -24
     return rel * mass + u * np.abs(out) * 1.01 + tiny, d[..., 0] + 2.0 ** -18
+
+
+def attention_scored(q, k, v, table, lens, cu, T, scale, causal, softcap=0.0, slopes=None, first=None, prefix=None,
+                     scale_ratio=1.0):
+    """attention() of capped and biased scores under document and prefix masks:
+    (out, lse, bound of |out - exact| before its last rounding, bound of |lse -
+    exact|).
+
+    A key's score is off by e (natural units): D exact products summed in fp32
+    and two products ((D + 4) 2^-23 of their magnitudes), the cap (2^-20 softcap,
+    or 2^-18 of the score where softcap passes 350), the bias and the subtraction
+    of the maximum (2^-22 of the magnitudes of score, bias and maximum, each
+    rounded a few times at 2^-24), the exponential (2^-20).  e's mean under the
+    probabilities enters numerator and denominator; attention_bounds has the rest.
+    A probability enters the second product in fp16, 2^11 above its quotient with
+    the row's largest: where that is below fp16's normal numbers its steps are
+    2^-24, so it is off by half of one, 2^-36 of the largest (at most 1), times the
+    ratio of the largest value scale to its page's and 2, by which the reference
+    of the scales may lag.  Summed over the keys, that stands where a row's
+    probability lies on a key whose value is 0."""
+    tokens, H, D = q.shape
+    G = H // k.shape[1]
+    out, mass, emass = np.zeros((tokens, H, D)), np.zeros((tokens, H, D)), np.zeros((tokens, H, D))
+    lse, e1 = np.full((tokens, H), -np.inf), np.zeros((tokens, H))
+    low = np.zeros((tokens, H, D))
+    for b in range(len(lens)):
+        n = cu[b + 1] - cu[b]
+        if lens[b] <= 0:
+            continue
+        pages = [table[b][p] for p in range(-(-lens[b] // T))]
+        kk = k[pages].transpose(1, 0, 2, 3).reshape(k.shape[1], -1, D)[:, :lens[b]]
+        vv = v[pages].transpose(1, 0, 2, 3).reshape(k.shape[1], -1, D)[:, :lens[b]]
+        for j in range(n):
+            t, p = cu[b] + j, lens[b] - n + j
+            hi = min(lens[b], (max(p + 1, prefix[b] if prefix is not None else 0) if p >= 0 else 0) if causal else lens[b])
+            lo = max(first[t], 0) if first is not None else 0
+            if lo >= hi:
+                continue
+            dist = np.abs(p - np.arange(lo, hi)).astype(np.float64)
+            for h in range(H):
+                x = q[t, h].astype(np.float64)
+                keys, vals = kk[h // G, lo:hi], vv[h // G, lo:hi]
+                s = keys @ x * scale
+                e = (D + 4) * 2.0 ** -23 * (np.abs(keys) @ np.abs(x)) * abs(scale) + 2.0 ** -20
+                if softcap:
+                    e = e + (2.0 ** -20 * softcap if softcap <= 350 else 2.0 ** -18 * np.abs(s))
+                    s = softcap * np.tanh(s / softcap)
+                bias = dist * slopes[h] if slopes is not None else 0.0 * dist
+                e = e + 2.0 ** -22 * (np.abs(s) + np.abs(bias))
+                s = s - bias
+                m = s.max()
+                e = e + 2.0 ** -22 * abs(m)
+                w = np.exp(s - m)
+                z = w.sum()
+                w = w / z
+                out[t, h], mass[t, h], emass[t, h] = w @ vals, w @ np.abs(vals), (w * e) @ np.abs(vals)
+                lse[t, h], e1[t, h] = m + np.log(z), w @ e
+                low[t, h] = 2.0 ** -35 * scale_ratio * np.abs(vals).sum(0)
+    seen = np.asarray(lens).max() if len(lens) else 0
+    rest = 2.0 ** -11 + (80 + seen / 64) * 2.0 ** -22 + seen * 2.0 ** -24
+    return out, lse, (emass + e1[..., None] * mass) * 1.05 + rest * mass + low, e1 * 1.05 + 2.0 ** -18
+
+
+def rounded_bound(bound, out, dtype):
+    """bound, and the rounding to the output's type."""
+    u, tiny = (2.0 ** -11, 2.0 ** -25) if dtype == "f16" else (2.0 ** -8, 2.0 ** -134)
+    return bound * (1 + u) + u * np.abs(out) * 1.01 + tiny
