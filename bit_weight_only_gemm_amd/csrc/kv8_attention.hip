@@ -137,33 +137,25 @@ __device__ __forceinline__ float bent(float s, float cap, float per_cap) {
   return __builtin_fmaf(-2.0f * cap, r, cap);
 }
 __device__ __forceinline__ float bent_wide(float s, float cap, float per_cap) {
-  const float x = s / cap, y = x * x;
+  const float x = s * (per_cap * (0.5f / kLog2e)), y = x * x;
   float t = __builtin_fmaf(y, -17.0f / 315.0f, 2.0f / 15.0f);
   t = __builtin_fmaf(y, __builtin_fmaf(y, t, -1.0f / 3.0f), 1.0f);
   return fabsf(x) < 0.25f ? s * t : bent(s, cap, per_cap);
 }
 
-// The final scores of N tokens from t on, from products that are to be multiplied
-// by f.  back: the query's position less t.
-template <int N>
-__device__ __forceinline__ void scored(float (&s)[N], float f, const Scoring& sc, float slope,
-                                       float back) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) s[i] *= f;
-  if (sc.cap > 0.0f) {
-    const float per_cap = 2.0f * kLog2e / sc.cap;
-    if (sc.cap > kWideCap) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] = bent_wide(s[i], sc.cap, per_cap);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] = bent(s[i], sc.cap, per_cap);
-    }
-  }
-  if (sc.slopes) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = __builtin_fmaf(-slope, fabsf(back - (float)i), s[i]);
-  }
+// The final score of a token, from a product that is to be multiplied by f.  back:
+// the query's position less the token's.  Kernels are built for what they do to
+// scores: kMasks nothing, else kCap or kWide, and kBias.  (As branches at run time
+// these cost the prompt kernel more registers than it has: 30 ms instead of 2.)
+enum { kPlain = 0, kMasks = 1, kCap = 2, kWide = 4, kBias = 8 };
+template <int MODE>
+__device__ __forceinline__ float scored(float s, float f, float cap, float per_cap, float slope,
+                                        float back) {
+  s *= f;
+  if constexpr ((MODE & kCap) != 0) s = bent(s, cap, per_cap);
+  if constexpr ((MODE & kWide) != 0) s = bent_wide(s, cap, per_cap);
+  if constexpr ((MODE & kBias) != 0) s = __builtin_fmaf(-slope, fabsf(back), s);
+  return s;
 }
 
 // Units of a split: this sequence's in equal shares, none below the planned.
@@ -224,12 +216,13 @@ __device__ __forceinline__ float four_rows_max(float x) {
 // With 16 rows to a wave and not more, three waves share a SIMD and cover each
 // other's waits: 32 or 48 rows a wave read the codes less often, and took 27 us
 // against 21 for 24 sequences of 4001, 40 rows of 64 channels a kv head.
-template <int DT, int D, bool SCORED>
+template <int DT, int D, int MODE>
 __global__ void __launch_bounds__(256)
 kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float scale, int causal,
                   uint16_t* __restrict__ out, int64_t out_stride, float* __restrict__ lse,
                   Parts parts, int row_tiles, int splits, int units, Scoring sc) {
   constexpr int DC = D / 64, DN = D / 16;
+  constexpr bool SCORED = MODE != kPlain;
   __shared__ float joined[4][16][D + 4];
   __shared__ float stat[4][2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -265,7 +258,8 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     low_max = __builtin_amdgcn_readfirstlane(low_max);
     low_min = __builtin_amdgcn_readfirstlane(low_min);
   }
-  const float slope = SCORED && sc.slopes ? sc.slopes[head] * kLog2e : 0.0f;
+  const float slope = (MODE & kBias) != 0 ? sc.slopes[head] * kLog2e : 0.0f;
+  const float per_cap = 2.0f * kLog2e / sc.cap;
 
   // units nu0 .. nu - 1, this split's u0 .. u1 - 1
   const int top = tile_limit(seq, causal, rt, 16, G, prefix);
@@ -361,12 +355,10 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
                       (!SCORED || t0 + (whole ? 63 : 16 * g + 15) >= low_min);
     float f = held ? f_row * ks : 0.0f;
     if constexpr (SCORED) {
-      float t[16];
+      const float back = (float)(seq.first + ridx / G - t0 - 16 * g);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = s[i >> 2][i & 3];
-      scored(t, f, sc, slope, (float)(seq.first + ridx / G - t0 - 16 * g));
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] = t[i];
+      for (int i = 0; i < 16; ++i)
+        s[i >> 2][i & 3] = scored<MODE>(s[i >> 2][i & 3], f, sc.cap, per_cap, slope, back - (float)i);
       f = 1.0f;
     } else if (f == 0.0f) {
       f = 1e-37f;  // a hidden key stays at -inf
@@ -571,7 +563,7 @@ __device__ __forceinline__ int swizzle(int row) {
 template <int D>
 constexpr int kPromptWaves = D / 16;
 
-template <int DT, int D, bool WHOLE, bool SCORED>
+template <int DT, int D, bool WHOLE, int MODE>
 __global__ void __launch_bounds__(64 * kPromptWaves<D>) __attribute__((amdgpu_waves_per_eu(1, 2)))
 kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float scale, int causal,
                   uint16_t* __restrict__ out, int64_t out_stride, float* __restrict__ lse,
@@ -579,6 +571,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   // in iteration u the keys of u + 1 and the values of u are read, and both of
   // u + 2 written
   constexpr int NBK = 2, NBV = 3, W = kPromptWaves<D>;
+  constexpr bool SCORED = MODE != kPlain;
   constexpr int KS = D / 16, DN = D / 32, ROWS = 32 * W;
   constexpr int BUF = kUnit * D * 2;                // fp16 keys (or values) of a unit
   static_assert(kUnit * D == 64 * W * 16, "a 16-byte piece of each for every lane");
@@ -630,7 +623,10 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       low_min = __builtin_amdgcn_readfirstlane(low_min);
     }
   }
-  const float slope = SCORED && sc.slopes ? sc.slopes[head] * kLog2e : 0.0f;
+  const float slope = (MODE & kBias) != 0 ? sc.slopes[head] * kLog2e : 0.0f;
+  const float per_cap = 2.0f * kLog2e / sc.cap;
+
+  const int position = seq.first + ridx / G;
 
   // units nu0 .. nu - 1, this split's u0 .. u1 - 1
   const int top = tile_limit(seq, causal, rt, ROWS, G, prefix);
@@ -774,13 +770,10 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     if constexpr (SCORED) {
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        float t[16];
+        const float back = (float)(position - t0 - 32 * a - 16 * h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = s[a][i];
-        scored(t, f[WHOLE ? 0 : a], sc, slope,
-               (float)(seq.first + ridx / G - t0 - 32 * a - 16 * h));
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[a][i] = t[i];
+        for (int i = 0; i < 16; ++i)
+          s[a][i] = scored<MODE>(s[a][i], f[WHOLE ? 0 : a], sc.cap, per_cap, slope, back - (float)i);
       }
 #pragma unroll
       for (int a = 0; a < NSC; ++a) f[a] = 1.0f;
@@ -920,24 +913,18 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   };
   int u = u0;
   if constexpr (SCORED) {
-    for (; u < u1; u += 2) {
-      if (u * kUnit >= low_max && u + 1 < u1 && (u + 2) * kUnit <= lim_all) {
-        turn(std::false_type{}, even, odd, u, 0);
-        turn(std::false_type{}, odd, even, u + 1, 1);
-      } else {
-        turn(std::true_type{}, even, odd, u, 0);
-        if (u + 1 < u1) turn(std::true_type{}, odd, even, u + 1, 1);
-      }
-    }
-  } else {
-    for (; u + 1 < u1 && (u + 2) * kUnit <= lim_all; u += 2) {
-      turn(std::false_type{}, even, odd, u, 0);
-      turn(std::false_type{}, odd, even, u + 1, 1);
-    }
-    for (; u < u1; u += 2) {
+    for (; u < u1 && u * kUnit < low_max; u += 2) {
       turn(std::true_type{}, even, odd, u, 0);
       if (u + 1 < u1) turn(std::true_type{}, odd, even, u + 1, 1);
     }
+  }
+  for (; u + 1 < u1 && (u + 2) * kUnit <= lim_all; u += 2) {
+    turn(std::false_type{}, even, odd, u, 0);
+    turn(std::false_type{}, odd, even, u + 1, 1);
+  }
+  for (; u < u1; u += 2) {
+    turn(std::true_type{}, even, odd, u, 0);
+    if (u + 1 < u1) turn(std::true_type{}, odd, even, u + 1, 1);
   }
   l += __shfl_xor(l, 32, 64);
 
@@ -975,7 +962,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
 
 // Joins the prompt kernel's splits of a row, in their order: one wave per
 // (token, head).
-template <int DT, int D, bool SCORED>
+template <int DT, int D, int MODE>
 __global__ void __launch_bounds__(256)
 kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_stride,
                 float* __restrict__ lse, Parts parts, int splits, int units, int rows, int max_new) {
@@ -986,6 +973,7 @@ kv8_join_kernel(Kv8 c, int causal, uint16_t* __restrict__ out, int64_t out_strid
   const int hd = (int)(i % c.H), j = (int)(i / c.H % max_new), b = (int)(i / c.H / max_new);
   const Kv8Seq seq = kv8_seq(c, b);
   if (j >= seq.n) return;
+  constexpr bool SCORED = MODE != kPlain;
   // (scored: every split has left its sum, those without units a 0)
   int n = splits;
   if constexpr (!SCORED) {
@@ -1056,7 +1044,7 @@ int64_t part_bytes(const Plan& p, int64_t tokens, int H, int D) {
   return kCounters * 4 + pad256(rows * D * 4) + pad256(rows * 8);
 }
 
-template <int DT, int D, bool SCORED>
+template <int DT, int D, int MODE>
 hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t q_stride,
                             float scale, int causal, void* out, int64_t out_stride, float* lse,
                             int64_t max_new, void* ws, const Scoring& sc, hipStream_t st) {
@@ -1071,11 +1059,11 @@ hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t 
   };
   const int64_t grid = 8 * ceil_div(groups, 8) * p.row_tiles;
   const bool whole = (1 << c.lgT) >= kUnit;
-  if (p.waves == 0) go(kv8_decode_kernel<DT, D, SCORED>, grid, 256);
-  else if (whole) go(kv8_prompt_kernel<DT, D, true, SCORED>, grid, 64 * kPromptWaves<D>);
-  else go(kv8_prompt_kernel<DT, D, false, SCORED>, grid, 64 * kPromptWaves<D>);
+  if (p.waves == 0) go(kv8_decode_kernel<DT, D, MODE>, grid, 256);
+  else if (whole) go(kv8_prompt_kernel<DT, D, true, MODE>, grid, 64 * kPromptWaves<D>);
+  else go(kv8_prompt_kernel<DT, D, false, MODE>, grid, 64 * kPromptWaves<D>);
   if (p.waves && p.splits > 1)
-    hipLaunchKernelGGL((kv8_join_kernel<DT, D, SCORED>),
+    hipLaunchKernelGGL((kv8_join_kernel<DT, D, MODE == kPlain ? kPlain : kMasks>),
                        dim3((unsigned)ceil_div((int64_t)c.B * max_new * c.H, 4)), dim3(256), 0,
                        st, c, causal, (uint16_t*)out, out_stride, lse, parts, p.splits, p.units, p.rows,
                        (int)max_new);
@@ -1087,8 +1075,15 @@ hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t 
 
 namespace w4a16 {
 namespace {
-template <bool SCORED>
-int attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+template <int MODE>
+auto launcher(int32_t D, int32_t dtype) {
+  return D == 64 ? (dtype == DT_F16 ? launch_attention<DT_F16, 64, MODE>
+                                    : launch_attention<DT_BF16, 64, MODE>)
+                 : (dtype == DT_F16 ? launch_attention<DT_F16, 128, MODE>
+                                    : launch_attention<DT_BF16, 128, MODE>);
+}
+
+int attention(int mode, const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
               const float* k_scale, const float* v_scale, int64_t num_pages, int32_t page_size,
               const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens,
               const int32_t* cu_seqlens, float scale, int32_t causal, const Scoring& sc, void* out,
@@ -1120,10 +1115,13 @@ int attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const uin
                    const_cast<float*>(k_scale), const_cast<float*>(v_scale), page_table, seq_lens,
                    cu_seqlens, (int)num_pages, (int)max_pages, (int)B, (int)tokens, (int)max_new, H,
                    Hkv, log2_page(page_size)};
-    auto* f = D == 64 ? (dtype == DT_F16 ? launch_attention<DT_F16, 64, SCORED>
-                                         : launch_attention<DT_BF16, 64, SCORED>)
-                      : (dtype == DT_F16 ? launch_attention<DT_F16, 128, SCORED>
-                                         : launch_attention<DT_BF16, 128, SCORED>);
+    auto* f = mode == kPlain             ? launcher<kPlain>(D, dtype)
+              : mode == kMasks            ? launcher<kMasks>(D, dtype)
+              : mode == (kMasks | kCap)   ? launcher<kMasks | kCap>(D, dtype)
+              : mode == (kMasks | kWide)  ? launcher<kMasks | kWide>(D, dtype)
+              : mode == (kMasks | kBias)  ? launcher<kMasks | kBias>(D, dtype)
+              : mode == (kMasks | kCap | kBias) ? launcher<kMasks | kCap | kBias>(D, dtype)
+                                          : launcher<kMasks | kWide | kBias>(D, dtype);
     return hip_status(f(c, p, q, q_stride, scale, causal, out, out_stride, lse, max_new, workspace,
                         sc, (hipStream_t)stream));
   });
@@ -1152,7 +1150,7 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
                   void* out, int64_t out_stride, float* lse, int64_t tokens, int64_t B,
                   int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
                   int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
-  return attention<false>(q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
+  return attention(kPlain, q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
                           page_table, max_pages, seq_lens, cu_seqlens, scale, causal, Scoring{},
                           out, out_stride, lse, tokens, B, max_new, max_len, H, Hkv, D, dtype,
                           workspace, workspace_bytes, stream);
@@ -1170,7 +1168,9 @@ int kv8_attention_scored(const void* q, int64_t q_stride, const uint8_t* k_cache
   // (beyond these the quotients of scores and cap leave fp32)
   if (softcap != 0.0f && !(softcap >= 1e-3f && softcap <= 1e30f)) return W4A16_ERR_INVALID_ARG;
   const Scoring sc = {softcap * kLog2e, slopes, first, prefix};
-  return attention<true>(q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
+  const int mode = kMasks | (sc.cap == 0.0f ? 0 : sc.cap <= kWideCap ? kCap : kWide) |
+                   (slopes ? kBias : 0);
+  return attention(mode, q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
                          page_table, max_pages, seq_lens, cu_seqlens, scale, causal, sc, out,
                          out_stride, lse, tokens, B, max_new, max_len, H, Hkv, D, dtype, workspace,
                          workspace_bytes, stream);
