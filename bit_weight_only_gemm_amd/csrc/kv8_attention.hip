@@ -120,42 +120,92 @@ __device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, i
 // value before the maximum is taken, so that everything after it goes by them
 // with a factor of 1.
 struct Scoring {
-  float cap;
+  float cap, per_cap;     // and 1 / cap
   const float* slopes;    // [H] or null
   const int32_t* first;   // [tokens] or null
   const int32_t* prefix;  // [B] or null
 };
 
-// tanh(x) = 1 - 2 / (1 + exp(2 x)): one exponential and one reciprocal of 1 ulp and
-// three roundings, together 2^-20 off at most, which the cap multiplies: 5e-5 of a
-// probability under a cap of 50, where its rounding to fp16 is 5e-4.  Under larger
-// caps small scores are bent by the series instead (x - x^3 / 3 + 2 x^5 / 15 - 17 x^7
-// / 315, 2^-21 of itself off at 1 / 4), so that the error stays a part of the score.
-constexpr float kWideCap = 512.0f;
-__device__ __forceinline__ float bent(float s, float cap, float per_cap) {
-  const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s * per_cap));
-  return __builtin_fmaf(-2.0f * cap, r, cap);
+// Kernels are built for what they do to scores: kMasks nothing, else kCap or kWide,
+// and kBias.  (As branches at run time these cost the prompt kernel more registers
+// than it has: 30 ms instead of 1.6.)
+//
+// tanh(x) = 1 - 2 / (1 + exp(2 x)), an exponential and a reciprocal of 1 ulp and
+// three roundings, is 2^-20 off at most, which the cap multiplies: 5e-5 of a
+// probability under a cap of 50, where its rounding to fp16 is 5e-4.  x P(x^2), P a
+// fit of degree 4 to tanh(x) / x over |x| < 3 / 4, is 9e-7 of itself off (2^-20) and
+// costs 28 cycles a wave and score instead of 44: a unit whose scores are all that
+// small under their cap takes it.  Under caps beyond kWideCap every small score does,
+// so that the error stays a part of the score.
+enum { kPlain = 0, kMasks = 1, kCap = 2, kWide = 4, kBias = 8 };
+constexpr float kWideCap = 512.0f, kBend = 0.75f;
+
+__device__ __forceinline__ float tanh_near(float x) {
+  const float y = x * x;
+  float p = __builtin_fmaf(y, 0.012918088f, -0.050102882f);
+  p = __builtin_fmaf(y, p, 0.132636398f);
+  p = __builtin_fmaf(y, p, -0.333293557f);
+  return x * __builtin_fmaf(y, p, 0.99999994f);
 }
-__device__ __forceinline__ float bent_wide(float s, float cap, float per_cap) {
-  const float x = s * (per_cap * (0.5f / kLog2e)), y = x * x;
-  float t = __builtin_fmaf(y, -17.0f / 315.0f, 2.0f / 15.0f);
-  t = __builtin_fmaf(y, __builtin_fmaf(y, t, -1.0f / 3.0f), 1.0f);
-  return fabsf(x) < 0.25f ? s * t : bent(s, cap, per_cap);
+__device__ __forceinline__ float tanh_any(float twice_x_log2e) {
+  const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(twice_x_log2e));
+  return __builtin_fmaf(-2.0f, r, 1.0f);
 }
 
-// The final score of a token, from a product that is to be multiplied by f.  back:
-// the query's position less the token's.  Kernels are built for what they do to
-// scores: kMasks nothing, else kCap or kWide, and kBias.  (As branches at run time
-// these cost the prompt kernel more registers than it has: 30 ms instead of 2.)
-enum { kPlain = 0, kMasks = 1, kCap = 2, kWide = 4, kBias = 8 };
-template <int MODE>
-__device__ __forceinline__ float scored(float s, float f, float cap, float per_cap, float slope,
-                                        float back) {
-  s *= f;
-  if constexpr ((MODE & kCap) != 0) s = bent(s, cap, per_cap);
-  if constexpr ((MODE & kWide) != 0) s = bent_wide(s, cap, per_cap);
-  if constexpr ((MODE & kBias) != 0) s = __builtin_fmaf(-slope, fabsf(back), s);
-  return s;
+// The scores of N groups of 16 tokens from products that are to be multiplied by
+// f[a]; back[a]: the query's position less the group's first token.  Afterwards f[a]
+// is what they are still to be multiplied by: the cap, or 1 where a bias came on.
+template <int MODE, int N>
+__device__ __forceinline__ void put_on(float (&s)[N][16], float (&f)[N], const Scoring& sc,
+                                       float slope, const float (&back)[N]) {
+  constexpr bool CAPPED = (MODE & (kCap | kWide)) != 0, BIAS = (MODE & kBias) != 0;
+  if constexpr (CAPPED) {
+    float to_x[N];
+#pragma unroll
+    for (int a = 0; a < N; ++a) to_x[a] = f[a] * sc.per_cap;
+    if constexpr ((MODE & kWide) != 0) {
+#pragma unroll
+      for (int a = 0; a < N; ++a)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = s[a][i] * to_x[a];
+          s[a][i] = fabsf(x) < kBend ? tanh_near(x) : tanh_any(x * (2.0f * kLog2e));
+        }
+    } else {
+      float most = 0.0f;
+#pragma unroll
+      for (int a = 0; a < N; ++a) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) t = fmaxf(fmaxf(t, fabsf(s[a][i])), fabsf(s[a][i + 1]));
+        most = fmaxf(most, t * to_x[a]);
+      }
+      if (__all(most < kBend)) {
+#pragma unroll
+        for (int a = 0; a < N; ++a)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[a][i] = tanh_near(s[a][i] * to_x[a]);
+      } else {
+#pragma unroll
+        for (int a = 0; a < N; ++a) {
+          const float z = to_x[a] * (2.0f * kLog2e);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[a][i] = tanh_any(s[a][i] * z);
+        }
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < N; ++a) f[a] = sc.cap;
+  }
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int a = 0; a < N; ++a) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        s[a][i] = __builtin_fmaf(s[a][i], f[a], -(slope * fabsf(back[a] - (float)i)));
+      f[a] = 1.0f;
+    }
+  }
 }
 
 // Units of a split: this sequence's in equal shares, none below the planned.
@@ -259,7 +309,6 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     low_min = __builtin_amdgcn_readfirstlane(low_min);
   }
   const float slope = (MODE & kBias) != 0 ? sc.slopes[head] * kLog2e : 0.0f;
-  const float per_cap = 2.0f * kLog2e / sc.cap;
 
   // units nu0 .. nu - 1, this split's u0 .. u1 - 1
   const int top = tile_limit(seq, causal, rt, 16, G, prefix);
@@ -354,15 +403,16 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     const bool held = (whole || t0 + 16 * g < seq.len) &&
                       (!SCORED || t0 + (whole ? 63 : 16 * g + 15) >= low_min);
     float f = held ? f_row * ks : 0.0f;
-    if constexpr (SCORED) {
-      const float back = (float)(seq.first + ridx / G - t0 - 16 * g);
+    if constexpr ((MODE & ~kMasks) != 0) {
+      float t[1][16], factor[1] = {f};
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        s[i >> 2][i & 3] = scored<MODE>(s[i >> 2][i & 3], f, sc.cap, per_cap, slope, back - (float)i);
-      f = 1.0f;
-    } else if (f == 0.0f) {
-      f = 1e-37f;  // a hidden key stays at -inf
+      for (int i = 0; i < 16; ++i) t[0][i] = s[i >> 2][i & 3];
+      put_on<MODE>(t, factor, sc, slope, {(float)(seq.first + ridx / G - t0 - 16 * g)});
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] = t[0][i];
+      f = factor[0];
     }
+    if (f == 0.0f) f = 1e-37f;  // a hidden key stays at -inf
     const float v_scale = held ? vs : 0.0f;
     const float vs_top = whole ? v_scale : four_rows_max(v_scale);
     // rows past the tile's last see what the others do; they are not written
@@ -582,13 +632,23 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, h = lane >> 5;
   // workgroups go to the 8 XCDs in turn: all row tiles of one (split, sequence,
-  // kv head) go to one of them and share their keys in its cache; the last
-  // tiles, which see the most, first
-  const int groups = c.B * c.Hkv * splits, per_xcd = (groups + 7) >> 3;
-  const int at = (int)(blockIdx.x >> 3);
-  const int grp = at % per_xcd * 8 + (int)(blockIdx.x & 7);
-  if (grp >= groups) return;
-  const int rt = row_tiles - 1 - at / per_xcd;
+  // kv head) go to one of them and share their keys in its cache; those of the
+  // groups that are left when each has as many go to all of them, so that none
+  // waits for the others (12 groups of 251 tiles, packed documents: 600 us -> 472);
+  // the last tiles, which see the most, first
+  const int groups = c.B * c.Hkv * splits, per_xcd = groups >> 3, rest = groups & 7;
+  const int shared = (rest * row_tiles + 7) >> 3;  // workgroups of an XCD for those
+  int at = (int)(blockIdx.x >> 3), grp, rt;
+  if (at < shared) {
+    const int i = at * 8 + (int)(blockIdx.x & 7);
+    if (i >= rest * row_tiles) return;
+    grp = per_xcd * 8 + i % rest;
+    rt = row_tiles - 1 - i / rest;
+  } else {
+    at -= shared;
+    grp = at % per_xcd * 8 + (int)(blockIdx.x & 7);
+    rt = row_tiles - 1 - at / per_xcd;
+  }
   const int hk = grp % c.Hkv, b = grp / c.Hkv % c.B, split = grp / c.Hkv / c.B;
   const int G = c.H / c.Hkv;
   const Kv8Seq seq = kv8_seq(c, b);
@@ -624,7 +684,6 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     }
   }
   const float slope = (MODE & kBias) != 0 ? sc.slopes[head] * kLog2e : 0.0f;
-  const float per_cap = 2.0f * kLog2e / sc.cap;
 
   const int position = seq.first + ridx / G;
 
@@ -764,20 +823,22 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
                         (!SCORED || t0 + (WHOLE ? 63 : 32 * a + 16 * h + 15) >= low_wave);
       f[a] = held ? f_row * ks_next[a] : 0.0f;
       vs[a] = held ? vs_next[a] : 0.0f;
-      if (!SCORED && f[a] == 0.0f) f[a] = 1e-37f;  // a hidden key stays at -inf
     }
     auto hidden = [&](int l) { return l >= lim || (SCORED && l < low); };
-    if constexpr (SCORED) {
+    if constexpr ((MODE & ~kMasks) != 0) {
+      float t[2][16], factor[2] = {f[0], f[NSC - 1]};
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const float back = (float)(position - t0 - 32 * a - 16 * h);
+      for (int i = 0; i < 32; ++i) t[i >> 4][i & 15] = s[i >> 4][i & 15];
+      const float back = (float)(position - t0 - 16 * h);
+      put_on<MODE>(t, factor, sc, slope, {back, back - 32.0f});
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[a][i] = scored<MODE>(s[a][i], f[WHOLE ? 0 : a], sc.cap, per_cap, slope, back - (float)i);
-      }
+      for (int i = 0; i < 32; ++i) s[i >> 4][i & 15] = t[i >> 4][i & 15];
 #pragma unroll
-      for (int a = 0; a < NSC; ++a) f[a] = 1.0f;
+      for (int a = 0; a < NSC; ++a) f[a] = factor[a];
     }
+#pragma unroll
+    for (int a = 0; a < NSC; ++a)
+      if (f[a] == 0.0f) f[a] = 1e-37f;  // a hidden key stays at -inf
     vs_top = vs[0];
     if constexpr (!WHOLE) vs_top = both_halves_max(fmaxf(vs[0], vs[1]));
     // ---- the rows' maxima
@@ -1057,7 +1118,8 @@ hipError_t launch_attention(const Kv8& c, const Plan& p, const void* q, int64_t 
                  q_stride, scale, causal, (uint16_t*)out, out_stride, lse, parts, p.row_tiles,
                  p.splits, p.units, sc);
   };
-  const int64_t grid = 8 * ceil_div(groups, 8) * p.row_tiles;
+  const int64_t grid = p.waves ? 8 * (groups / 8 * p.row_tiles + ceil_div(groups % 8 * p.row_tiles, 8))
+                               : 8 * ceil_div(groups, 8) * p.row_tiles;
   const bool whole = (1 << c.lgT) >= kUnit;
   if (p.waves == 0) go(kv8_decode_kernel<DT, D, MODE>, grid, 256);
   else if (whole) go(kv8_prompt_kernel<DT, D, true, MODE>, grid, 64 * kPromptWaves<D>);
@@ -1167,7 +1229,8 @@ int kv8_attention_scored(const void* q, int64_t q_stride, const uint8_t* k_cache
                          int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
   // (beyond these the quotients of scores and cap leave fp32)
   if (softcap != 0.0f && !(softcap >= 1e-3f && softcap <= 1e30f)) return W4A16_ERR_INVALID_ARG;
-  const Scoring sc = {softcap * kLog2e, slopes, first, prefix};
+  const float cap = softcap * kLog2e;
+  const Scoring sc = {cap, 1.0f / cap, slopes, first, prefix};
   const int mode = kMasks | (sc.cap == 0.0f ? 0 : sc.cap <= kWideCap ? kCap : kWide) |
                    (slopes ? kBias : 0);
   return attention(mode, q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
