@@ -8,8 +8,8 @@
 // whatever the order its atomics (sums of integers) happen in.
 //
 // A call that takes pages is planned by one workgroup, which goes through refs
-// once or twice (4 KB to 600 KB: a pool of 288 GB in pages of 128 KB for each of
-// 16 layers has 140 000 pages), and carried out by a second launch.
+// once or twice, 16 KB at a time (a pool of 288 GB in pages of 128 KB for each of 16
+// layers has 140 000 pages, 560 KB), and carried out by a second launch.
 #include <algorithm>
 
 #include "kv8.h"
@@ -73,15 +73,37 @@ __device__ __forceinline__ int before_me(int v, int* part, int& total) {
   return (int)(lane ? plus(base, mine) : base);
 }
 
+// Counters of the four pages from 4 (turn * kPlan + lane) on: a turn of the planning
+// workgroup.  Past the pool's end they are `beyond`.
+constexpr int kTurn = 4 * kPlan;
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4_t counters(const Pool& p, int64_t at, int beyond) {
+  const int64_t page = at + 4 * (int)threadIdx.x;
+  i32x4_t n = {beyond, beyond, beyond, beyond};
+  if (page + 4 <= p.pages) {
+    n = *(const i32x4_t*)(p.refs + page);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (page + i < p.pages) n[i] = p.refs[page + i];
+  }
+  return n;
+}
+
 // Lists the lowest free pages, as many as wanted; how many there are of those.
 __device__ int list_free(const Pool& p, int wanted, int32_t* list, int* part) {
   int found = 0;
-  for (int at = 0; at < p.pages && found < wanted; at += kPlan) {
-    const int page = at + (int)threadIdx.x;
-    const bool free = page < p.pages && p.refs[page] == 0;
-    int total;
-    const int rank = found + before_me(free, part, total);
-    if (free && rank < wanted) list[rank] = page;
+  i32x4_t next = counters(p, 0, 1);
+  for (int64_t at = 0; at < p.pages && found < wanted; at += kTurn) {
+    const i32x4_t n = next;
+    next = counters(p, at + kTurn, 1);  // a turn ahead
+    int total, rank = found;
+    rank += before_me((n[0] == 0) + (n[1] == 0) + (n[2] == 0) + (n[3] == 0), part, total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (n[i] == 0 && rank < wanted) list[rank] = (int)at + 4 * (int)threadIdx.x + i;
+      rank += n[i] == 0;
+    }
     found += total;
   }
   __syncthreads();  // the list is whole
@@ -304,26 +326,39 @@ kv8_compact_plan_kernel(Pool p, int32_t* refs_out, int32_t* __restrict__ used_ou
   const int tid = threadIdx.x;
   int32_t *move = ws + 4, *hole = move + p.pages, *to = hole + p.pages;
   int count = 0;
-  for (int page = tid; page < p.pages; page += kPlan) count += p.refs[page] > 0;
+#pragma unroll 4
+  for (int64_t at = 0; at < p.pages; at += kTurn) {
+    const i32x4_t n = counters(p, at, 0);
+    count += (n[0] > 0) + (n[1] > 0) + (n[2] > 0) + (n[3] > 0);
+  }
   int used;
   before_me(count, part, used);
   int moves = 0, holes = 0;
-  for (int at = 0; at < p.pages; at += kPlan) {
-    const int page = at + tid;
-    const int n = page < p.pages ? p.refs[page] : 0;
-    const bool is_move = page < p.pages && page >= used && n > 0;
-    const bool is_hole = page < used && n <= 0;
-    int total;
-    int rank = before_me(is_move, part, total) + moves;
-    if (is_move) move[rank] = page;
-    moves += total;
-    rank = before_me(is_hole, part, total) + holes;
-    if (is_hole) hole[rank] = page;
-    holes += total;
-    if (page < p.pages) {
-      refs_out[page] = n;
-      to[page] = page;
+  i32x4_t next = counters(p, 0, 0);
+  for (int64_t at = 0; at < p.pages; at += kTurn) {
+    const i32x4_t n = next;
+    next = counters(p, at + kTurn, 0);  // a turn ahead
+    const int page = (int)at + 4 * tid;
+    // moves in the low half, holes in the high one: at most kTurn of either
+    int mine = 0, total;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      mine += page + i >= used ? n[i] > 0 : n[i] <= 0 ? 0x10000 : 0;
+    const int before = before_me(mine, part, total);
+    int rank_move = moves + (before & 0xFFFF), rank_hole = holes + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (page + i >= p.pages) break;
+      if (page + i >= used) {
+        if (n[i] > 0) move[rank_move++] = page + i;
+      } else if (n[i] <= 0) {
+        hole[rank_hole++] = page + i;
+      }
+      refs_out[page + i] = n[i];
+      to[page + i] = page + i;
     }
+    moves += total & 0xFFFF;
+    holes += total >> 16;
   }
   __syncthreads();
   for (int i = tid; i < moves; i += kPlan) {

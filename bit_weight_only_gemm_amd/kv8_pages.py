@@ -74,7 +74,7 @@ def _rows(page_table, seq_lens):
 
 def _status(status, like, stream):
     if status is None:
-        return _empty((1,), torch.int32, like.device, stream)
+        return like.new_empty(1) if stream is None else _empty((1,), torch.int32, like.device, stream)
     _need(status, torch.int32, "status", 1)
     return status
 
