@@ -405,8 +405,8 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   }
 }
 
-// The same product for many tokens: workgroups stay and take 256 x 256 tiles
-// in turn, 4 waves of 4 x 4 products.  K goes by in steps of 128 codes (whole
+// The same product for many tokens: workgroups stay and take 64 MT x 256 tiles
+// in turn, 4 waves of 4 x MT products (MT = 4, and 3 in the gated form).  K goes by in steps of 128 codes (whole
 // 128-byte lines of w and x), four quarters of 32 each:
 //
 //  * The rows of step t + 2 are loaded into registers while step t runs, each
@@ -432,13 +432,13 @@ constexpr int kWideStage = 512 * 128, kWideTurn = 2 * kWideStage, kWideScales = 
 // x's scales, w's, the bias as fp32; of this tile and of the one before
 constexpr int kWideLds = kWideScales + 2 * 256 * 12;
 
-template <int DT, int ACT>
+template <int DT, int ACT, int MT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
                  const int8_t* __restrict__ wq, const float* __restrict__ sw,
                  const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
                  int K, int mb, int nb, int per_xcd, Gate gate) {
-  constexpr int HALVES = ACT ? 2 : 1;
+  constexpr int HALVES = ACT ? 2 : 1, BM = 64 * MT, LOADS = 8 + 2 * MT;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWideLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -455,16 +455,17 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   auto tile_at = [&](int at, int& row0, int& col0) {
     const int band = at / (8 * nb), in_band = at % (8 * nb);
     const int bh = min(8, mb - band * 8);
-    row0 = (band * 8 + in_band % bh) * 256;
+    row0 = (band * 8 + in_band % bh) * BM;
     col0 = in_band / bh * 256;
   };
 
   // ---- loads: instruction i of a step fetches 8 rows x 128 bytes, i < 8 rows
-  // of w and i >= 8 rows of x, of rows 64 wave + 8 (i & 7) of the tile
+  // of w, from 64 wave + 8 i of the tile, i >= 8 rows of x, from 16 MT wave + 8 (i - 8)
   const int lrow = lane >> 3, lchunk = lane & 7;
   // (gated: block 8 wave + i of w is the block (8 wave + i) / 2 of the gate's rows
   // where i is even, of the up projection's where it is odd)
   const uint32_t lane_off = (uint32_t)(64 * wave + lrow) * (uint32_t)K + 16u * lchunk;
+  const uint32_t x_off = (uint32_t)(16 * MT * wave + lrow) * (uint32_t)K + 16u * lchunk;
   const uint32_t gate_off = (uint32_t)(32 * wave + lrow) * (uint32_t)K + 16u * lchunk;
   const uint32_t tail = 128 * (KT - 1) + 16 * lchunk >= K ? kOutOfRange : 0u;
   const uint32_t lane_lds = (uint32_t)(64 * wave + lrow) * 128 + 16u * (lchunk ^ ((lrow >> 1) & 3));
@@ -477,14 +478,15 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     const uint32_t w_bytes = any ? (uint32_t)min(256, N - col0) / HALVES * (uint32_t)K : 0u;
     rw = make_rsrc(wq + (size_t)(col0 / HALVES) * K, w_bytes);
     if constexpr (ACT != kNoGate) ru = make_rsrc(wq + (size_t)(gate.F + col0 / 2) * K, w_bytes);
-    rx = make_rsrc(xq + (size_t)row0 * K, any ? (uint32_t)min(256, M - row0) * (uint32_t)K : 0u);
+    rx = make_rsrc(xq + (size_t)row0 * K, any ? (uint32_t)min(BM, M - row0) * (uint32_t)K : 0u);
   };
   aim();
-  i32x4_t held[16];
+  i32x4_t held[LOADS];
   auto load = [&](int i) {
     const bool half = ACT && i < 8;
     const uint32_t row = half ? 8 * (i >> 1) : 8 * (i & 7);
-    const uint32_t off = ((half ? gate_off : lane_off) + row * (uint32_t)K) | (lt == KT - 1 ? tail : 0u);
+    const uint32_t base = half ? gate_off : i < 8 ? lane_off : x_off;
+    const uint32_t off = (base + row * (uint32_t)K) | (lt == KT - 1 ? tail : 0u);
     held[i] = __builtin_bit_cast(i32x4_t, bld128(i >= 8 ? rx : half && (i & 1) ? ru : rw, off, lt * 128));
   };
   auto loaded = [&]() {  // every load of a step is out
@@ -494,37 +496,39 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
       aim();
     }
   };
-  // row 64 wave + 8 i + lrow: (row >> 1) & 7 is ((lrow >> 1) & 3) + 4 (i & 1)
+  // row 64 wave + 8 i + lrow (of x 16 MT wave + ..): (row >> 1) & 7 is ((lrow >> 1) &
+  // 3) + 4 (i & 1)
   auto store = [&](int slot, int i) {
-    *(i32x4_t*)(lds + slot * kWideStage + (i < 8 ? 0 : 32768) + (i & 7) * 1024 +
-                (lane_lds ^ ((i & 1) << 6))) = held[i];
+    *(i32x4_t*)(lds + slot * kWideStage + (i < 8 ? 0 : 32768 - (64 - 16 * MT) * 128 * wave) +
+                (i & 7) * 1024 + (lane_lds ^ ((i & 1) << 6))) = held[i];
   };
 
   const int r = lane & 31, h = lane >> 5;
-  i32x4_t fw[2][4], fx[2][4];
-  auto read = [&](int slot, int quarter, i32x4_t (&w)[4], i32x4_t (&x)[4]) {
+  i32x4_t fw[2][4], fx[2][MT];
+  auto read = [&](int slot, int quarter, i32x4_t (&w)[4], i32x4_t (&x)[MT]) {
     const uint8_t* st = lds + slot * kWideStage + (((2 * quarter + h) ^ ((r >> 1) & 7)) << 4) + r * 128;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = *(const i32x4_t*)(st + wn * 16384 + i * 4096);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *(const i32x4_t*)(st + 32768 + wm * 16384 + i * 4096);
+    for (int i = 0; i < MT; ++i) x[i] = *(const i32x4_t*)(st + 32768 + wm * MT * 4096 + i * 4096);
   };
-  i32x16_t acc[4][4];
-  auto products = [&](const i32x4_t (&w)[4], const i32x4_t (&x)[4], bool anew) {
+  i32x16_t acc[4][MT];
+  auto products = [&](const i32x4_t (&w)[4], const i32x4_t (&x)[MT], bool anew) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < MT; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], x[j], anew ? i32x16_t{} : acc[i][j],
                                                           0, 0, 0);
   };
-  // one quarter: 16 products, and between them 8 reads, `n` stores from
+  // one quarter: 4 MT products, and between them 4 + MT reads, `n` stores from
   // registers each followed by its load
   auto order = [&](auto n) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < 4 * MT; ++k) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (k < 4) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      if (k < MT) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      else if (k < 4) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       else if (2 * (k - 4) < 2 * decltype(n)::value && k - 4 < decltype(n)::value) {
         __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
@@ -535,12 +539,12 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 
   // ---- the first step goes to LDS, the second to registers
 #pragma unroll
-  for (int i = 0; i < 16; ++i) load(i);
+  for (int i = 0; i < LOADS; ++i) load(i);
   loaded();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) store(0, i);
+  for (int i = 0; i < LOADS; ++i) store(0, i);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) load(i);
+  for (int i = 0; i < LOADS; ++i) load(i);
   loaded();
   __syncthreads();
   read(0, 0, fw[0], fx[0]);
@@ -561,9 +565,9 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     order(std::integral_constant<int, 6>{});
     read(slot, 3, fw[1], fx[1]);
 #pragma unroll
-    for (int i = 12; i < 16; ++i) store(slot ^ 1, i), load(i);
+    for (int i = 12; i < LOADS; ++i) store(slot ^ 1, i), load(i);
     products(fw[0], fx[0], false);
-    order(std::integral_constant<int, 4>{});
+    order(std::integral_constant<int, LOADS - 12>{});
     loaded();
     if (decltype(anew)::value) {
       *scales_at(tid) = sx_v;
@@ -581,7 +585,7 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   for (int at = first; at < run1; at += every) {
     int row0, col0;
     tile_at(at, row0, col0);
-    sx_v = row0 + tid < M ? sx[row0 + tid] : 0.0f;
+    sx_v = tid < BM && row0 + tid < M ? sx[row0 + tid] : 0.0f;
     // (the channel of w's row tid of the tile)
     const int64_t ch = ACT ? (int64_t)col0 / 2 + (tid >> 4) * 8 + (tid & 7) + (tid & 8 ? gate.F : 0)
                            : col0 + tid;
@@ -593,7 +597,7 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
+      for (int j = 0; j < MT; ++j) asm volatile("" : "+a"(acc[i][j]));
 
     // ---- results: register e of product (i, j) is channel 8 (e >> 2) + 4 h +
     // (e & 3) of its 32, token lane & 31; blocks of 32 tokens x 64 channels of y, the
@@ -608,9 +612,9 @@ w8a8_wide_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     for (int i0 = 0; i0 < 4; i0 += 2 * HALVES) {
       const float* sn = scales_at(256 + wn * 128 + i0 * 32 + 4 * h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int mrow = row0 + (wm * 4 + j) * 32;
-        const float s = *scales_at((wm * 4 + j) * 32 + r);
+      for (int j = 0; j < MT; ++j) {
+        const int mrow = row0 + (wm * MT + j) * 32;
+        const float s = *scales_at((wm * MT + j) * 32 + r);
 #pragma unroll
         for (int i = 0; i < 2 * HALVES; ++i)
 #pragma unroll
@@ -1013,11 +1017,11 @@ void launch_stream(const Args& a, hipStream_t st) {
 // Whether w8a8_linear quantizes inside the product.
 bool fused(int64_t M, int64_t K) { return M * ceil_div(K, 4096) <= kRows; }
 
-template <int DT, int ACT>
+template <int DT, int ACT, int MT>
 void launch_wide(const Args& a, hipStream_t st) {
-  const int mb = (int)ceil_div(a.M, 256), nb = (int)ceil_div(a.N, 256);
+  const int mb = (int)ceil_div(a.M, 64 * MT), nb = (int)ceil_div(a.N, 256);
   const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
-  launch_timed(w8a8_wide_kernel<DT, ACT>, dim3((unsigned)std::min(256, per_xcd * 8)), dim3(256), 0, st,
+  launch_timed(w8a8_wide_kernel<DT, ACT, MT>, dim3((unsigned)std::min(256, per_xcd * 8)), dim3(256), 0, st,
                (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb, per_xcd,
                a.gate);
 }
@@ -1037,6 +1041,9 @@ void launch_wide(const Args& a, hipStream_t st) {
 //   16 x 4096 x 11008 12.5 / 24.6, 16 x 8192 x 4096 11.2 / 11.8,
 //   16 x 12288 x 4096 14.7 / 12.0, 32 x 4096 x 4096 8.8 / 11.6,
 //   32 x 8192 x 4096 14.5 / 11.7, 64 x 4096 x 4096 12.5 / 12.0
+// The gated form has tiles of 192 x 256 too, 1.4 us a round (192 / 256 rows, M x F x
+// K): 333 x 13824 x 5120 72.9 / 81.7, 1024 x 11008 x 4096 130 / 119; (192 / 128 rows)
+// 192 x 13824 x 5120 64.2 / 64.9, 384 x 13824 x 5120 69 / 98.
 template <int DT, int ACT>
 hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
   const int64_t t64 = ceil_div(a.M, 64) * ceil_div(a.N, 64);
@@ -1044,6 +1051,14 @@ hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
   const int64_t t256 = ceil_div(a.M, 256) * ceil_div(a.N, 256);
   const int64_t c64 = 3 * std::max<int64_t>(t64, 256), c128 = 6 * 256 * ceil_div(t128, 256),
                 c256 = 16 * 256 * ceil_div(t256, 256);
+  if constexpr (ACT != kNoGate) {
+    const int64_t t192 = ceil_div(a.M, 192) * ceil_div(a.N, 256);
+    const int64_t c192 = 14 * 256 * ceil_div(t192, 256);
+    if (c192 < c64 && c192 < c128 && c192 < c256) {
+      launch_wide<DT, ACT, 3>(a, st);
+      return hipGetLastError();
+    }
+  }
   if (!ACT && a.M <= 64 && ceil_div(a.M, 16) * a.N < 12288) {
     if (a.M > 32) launch_stream<DT, 4, 1, false>(a, st);
     else if (a.M > 16) launch_stream<DT, 2, 1, false>(a, st);
@@ -1053,7 +1068,7 @@ hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
   } else if (c128 <= c256) {
     launch_tile<DT, T128, ACT>(a, st);
   } else {
-    launch_wide<DT, ACT>(a, st);
+    launch_wide<DT, ACT, 4>(a, st);
   }
   return hipGetLastError();
 }

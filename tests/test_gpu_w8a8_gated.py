@@ -40,6 +40,7 @@ SHAPES = [  # M, F, K
     (100, 640, 1104), (129, 264, 5120), (255, 520, 1008),                                        # 64 x 64 tiles
     (333, 1792, 1280), (1000, 1016, 688), (512, 2568, 512),                                      # 128 x 128
     (2049, 2312, 320), (2304, 2304, 16), (8192, 2304, 144),                                      # 256 x 256
+    (333, 13832, 272), (1150, 4616, 144), (380, 27648, 64),                                      # 192 x 256
 ]
 
 
