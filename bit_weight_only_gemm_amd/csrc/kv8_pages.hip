@@ -111,31 +111,43 @@ __device__ int list_free(const Pool& p, int wanted, int32_t* list, int* part) {
 }
 
 // Bytes of chunk `chunk` of a page, keys and then values, and with the first
-// its scales.
-__device__ __forceinline__ void copy_chunk(const Layers& c, int layer, int64_t from, int64_t to,
-                                           int64_t kb, int Hkv, int chunk) {
+// its scales, read once and written to each page that to(..) names in turn, until
+// it names none (-1).
+template <class F>
+__device__ __forceinline__ void copy_chunk(const Layers& c, int layer, int64_t from, int64_t kb,
+                                           int Hkv, int chunk, F&& to) {
+  constexpr int N = kChunk / (256 * 16);
   const int tid = threadIdx.x;
-  u32x4_t w[4];
-  uint8_t* dst[4];
+  u32x4_t w[N];
+  uint8_t* dst[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int64_t off = (int64_t)chunk * kChunk + (i * 256 + tid) * 16;
     dst[i] = nullptr;
     if (off < 2 * kb) {
-      uint8_t* a = off < kb ? c.k[layer] : c.v[layer];
-      const int64_t in = off < kb ? off : off - kb;
-      w[i] = *(const u32x4_t*)(a + from * kb + in);
-      dst[i] = a + to * kb + in;
+      dst[i] = off < kb ? c.k[layer] + off : c.v[layer] + (off - kb);
+      w[i] = *(const u32x4_t*)(dst[i] + from * kb);
     }
   }
+  for (int64_t page = to(); page >= 0; page = to()) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (dst[i]) *(u32x4_t*)dst[i] = w[i];
-  if (chunk == 0)
-    for (int h = tid; h < Hkv; h += 256) {
-      c.ks[layer][to * Hkv + h] = c.ks[layer][from * Hkv + h];
-      c.vs[layer][to * Hkv + h] = c.vs[layer][from * Hkv + h];
-    }
+    for (int i = 0; i < N; ++i)
+      if (dst[i]) *(u32x4_t*)(dst[i] + page * kb) = w[i];
+    if (chunk == 0)
+      for (int h = tid; h < Hkv; h += 256) {
+        c.ks[layer][page * Hkv + h] = c.ks[layer][from * Hkv + h];
+        c.vs[layer][page * Hkv + h] = c.vs[layer][from * Hkv + h];
+      }
+  }
+}
+// To one page.
+__device__ __forceinline__ void copy_chunk(const Layers& c, int layer, int64_t from, int64_t to,
+                                           int64_t kb, int Hkv, int chunk) {
+  copy_chunk(c, layer, from, kb, Hkv, chunk, [next = to]() mutable {
+    const int64_t page = next;
+    next = -1;
+    return page;
+  });
 }
 
 // ------------------------------------------------------------------- copy ---
@@ -240,14 +252,17 @@ kv8_reserve_kernel(Pool p, const int32_t* __restrict__ added, int32_t* __restric
 
 // ------------------------------------------------------------------- fork ---
 // One workgroup: checks the rows and finds a page for every partly filled last
-// one.  ws: [n] that page's place in the list or -1, [n] the list, [B] marks.
+// one.  ws: [n] that page's place in the list or -1, [n] the list, [n] the next pair
+// of the same source or -1, [n] a pair of each source with such a page, from which the
+// others follow (in whatever order atomics come: all get the same bytes), [4] how many
+// those are, [B] marks of the rows.
 __global__ void __launch_bounds__(kPlan)
 kv8_fork_plan_kernel(Pool p, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n,
                      int32_t* __restrict__ status, int32_t* __restrict__ ws) {
   __shared__ int part[kWaves];
   __shared__ int bad;
   const int tid = threadIdx.x;
-  int32_t *place = ws, *list = ws + n, *marks = ws + 2 * (int64_t)n;
+  int32_t *place = ws, *list = ws + n, *link = list + n, *heads = link + n, *marks = heads + n + 4;
   if (tid == 0) bad = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kPlan) {
@@ -276,27 +291,40 @@ kv8_fork_plan_kernel(Pool p, const int32_t* __restrict__ src, const int32_t* __r
     if (i < n) place[i] = half ? wanted + rank : -1;
     wanted += total;
   }
-  const int found = list_free(p, wanted, list, part);
+  for (int i = tid; i < n; i += kPlan) marks[src[i]] = -1;
+  const int found = list_free(p, wanted, list, part);  // (and a barrier)
+  for (int i = tid; i < n; i += kPlan) link[i] = atomicExch(marks + src[i], i);
   if (found == wanted)
     for (int i = tid; i < wanted; i += kPlan) p.refs[list[i]] = 1;
-  if (tid == 0) *status = wanted - found;
+  __syncthreads();
+  int count = 0;
+  for (int at = 0; at < n; at += kPlan) {
+    const int i = at + tid;
+    const bool head = i < n && place[i] >= 0 && marks[src[i]] == i;
+    int total;
+    const int rank = before_me(head, part, total);
+    if (head) heads[count + rank] = i;
+    count += total;
+  }
+  if (tid == 0) {
+    heads[n] = count;
+    *status = wanted - found;
+  }
 }
 
-// The table's rows (by the first launch of a call: `rows`) and the copies.
+// The table's rows (by the first launch of a call: `rows`) and the copies, of each
+// source's last page to all of its children at once: 24 pages to 5 children each in 16
+// caches, 302 MB, took 79 us with a copy by each child, which reads 240 MB for 50.
 __global__ void __launch_bounds__(256)
 kv8_fork_kernel(Pool p, Layers c, int layers, const int32_t* __restrict__ src,
                 const int32_t* __restrict__ dst, int n, const int32_t* __restrict__ status,
                 const int32_t* __restrict__ ws, int rows, int64_t kb, int Hkv, int chunks) {
   if (*status != 0) return;
-  const int32_t *place = ws, *list = ws + n;
-  const int64_t per = (int64_t)layers * chunks + rows, items = per * n;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = (int)(it / per);
-    int64_t part = it % per - rows;
-    const int s = src[i], d = dst[i], len = len_of(p, s), whole = len >> p.lgT;
-    const int32_t* from = p.table + (int64_t)s * p.width;
-    const int fresh = place[i] < 0 ? -1 : list[place[i]];
-    if (part < 0) {
+  const int32_t *place = ws, *list = ws + n, *link = list + n, *heads = link + n;
+  if (rows)
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+      const int s = src[i], d = dst[i], len = len_of(p, s), whole = len >> p.lgT;
+      const int32_t* from = p.table + (int64_t)s * p.width;
       int32_t* to = p.table + (int64_t)d * p.width;
       for (int j = threadIdx.x; j < whole; j += 256) {
         const int page = from[j];
@@ -304,14 +332,21 @@ kv8_fork_kernel(Pool p, Layers c, int layers, const int32_t* __restrict__ src,
         if (valid(p, page)) atomicAdd(p.refs + page, 1);
       }
       if (threadIdx.x == 0) {
-        if (fresh >= 0) to[whole] = fresh;
+        if (place[i] >= 0) to[whole] = list[place[i]];
         p.lens[d] = len;
       }
-    } else if (fresh >= 0) {
-      const int page = from[whole];
-      if (valid(p, page))
-        copy_chunk(c, (int)(part / chunks), page, fresh, kb, Hkv, (int)(part % chunks));
     }
+  const int64_t per = (int64_t)layers * chunks, items = per * heads[n];
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int head = heads[it / per], part = (int)(it % per), s = src[head];
+    const int page = p.table[(int64_t)s * p.width + (len_of(p, s) >> p.lgT)];
+    if (!valid(p, page)) continue;
+    copy_chunk(c, part / chunks, page, kb, Hkv, part % chunks, [&, j = head]() mutable {
+      const int now = j;
+      if (now < 0) return -1;
+      j = link[now];
+      return list[place[now]];
+    });
   }
 }
 
@@ -427,7 +462,7 @@ int validate_pool(int64_t pages, int32_t T, int64_t width, int64_t B, int64_t n)
 
 // ints of workspace
 int64_t pages_ints(int64_t pages, int64_t B, int64_t n) {
-  return std::max(std::max(B + pages, B + 2 * n), 4 + 3 * pages);
+  return std::max(std::max(B + pages, B + 4 * n + 4), 4 + 3 * pages);
 }
 
 // Runs launch(layers, count of them, whether they are the call's first) on up
@@ -545,7 +580,7 @@ int kv8_fork(void* const* caches_host, int32_t count, int64_t num_pages, int32_t
                        status, ws);
     if (n == 0) return hip_status(hipGetLastError());
     each_layers(caches_host, count, [&](const Layers& c, int layers, bool first) {
-      hipLaunchKernelGGL(kv8_fork_kernel, groups_for(n * ((int64_t)layers * s.chunks + first)),
+      hipLaunchKernelGGL(kv8_fork_kernel, groups_for(n * (int64_t)layers * s.chunks),
                          dim3(256), 0, st, p, c, layers, src, dst, (int)n, status, ws, (int)first,
                          s.kb, Hkv, s.chunks);
     });

@@ -180,11 +180,13 @@ def kv8_attention_scored(q, cache, page_table, seq_lens, cu_seqlens=None, max_ne
     its document or of a window.  prefix (int32 [B]): with causal, positions below
     it are seen by every query of the sequence.  A query that sees nothing gives 0.
     The other arguments as for kv8_attention, its workspace among them."""
-    softcap = 0.0 if softcap is None else float(softcap)
-    extra = [softcap, None, None, None]
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, D]")
+    _need(seq_lens, torch.int32, "seq_lens")
+    extra = [0.0 if softcap is None else float(softcap), None, None, None]
     for i, (t, dtype, name, n) in enumerate(((slopes, torch.float32, "slopes", q.shape[1]),
                                              (first, torch.int32, "first", q.shape[0]),
-                                             (prefix, torch.int32, "prefix", seq_lens.shape[0]))):
+                                             (prefix, torch.int32, "prefix", seq_lens.numel()))):
         if t is not None:
             _need(t, dtype, name, n)
             extra[1 + i] = t.data_ptr()
@@ -214,8 +216,8 @@ def _attention(name, extra, q, cache, page_table, seq_lens, cu_seqlens, max_new,
     status = getattr(L, name)(
         q.data_ptr(), q_stride, *arrays, pages, T, page_table.data_ptr(), width,
         seq_lens.data_ptr(), cu, 1.0 / math.sqrt(D) if scale is None else float(scale),
-        1 if causal else 0, *(extra or ()), out.data_ptr(), o_stride, None if lse is None else lse.data_ptr(),
-        tokens, B, max_new, max_len, H, Hkv, D, _DT[dtype],
+        1 if causal else 0, *(extra or ()), out.data_ptr(), o_stride,
+        None if lse is None else lse.data_ptr(), tokens, B, max_new, max_len, H, Hkv, D, _DT[dtype],
         None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream))
     if status:
         _lib.check(status, name)

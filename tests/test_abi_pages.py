@@ -87,7 +87,7 @@ def test_what_only_one_call_takes():
 @pytest.mark.parametrize("call,n", [(reserve, 0), (fork, 2), (compact, 0)])
 def test_workspace(call, n):
     need = L.kv8_pages_workspace_bytes(8, 3, n)
-    assert need >= 4 * max(3 + 8, 3 + 2 * n)
+    assert need >= 4 * max(3 + 8, 7 + 4 * n)
     assert call(nbytes=need - 1) == WORKSPACE and call(space=NULL, nbytes=0) == WORKSPACE
     assert call(space=ODD) == MISALIGNED
 

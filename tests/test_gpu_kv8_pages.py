@@ -294,3 +294,33 @@ def test_refusals():
         w4.kv8_compact(caches, refs, table, lens, refs_out=torch.empty(5, dtype=torch.int32, device=DEV))
     with pytest.raises(w4.W4A16Error):
         w4.kv8_pages_workspace_bytes(0, 1)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages past 4 GB of keys are shared, copied and moved."""
+    T, Hkv, D, pages = 128, 32, 128, 9000
+    cache = w4.kv8_cache(pages, T, Hkv, D, DEV)
+    assert cache["k"].numel() > 1 << 32
+    refs, table, lens = ints([0] * pages), ints([[8990, 8995], [-1, -1], [-1, -1]]), ints([200, 0, 0])
+    refs[8990] = refs[8995] = 1
+    refs[2:8980] = 1                                # held by rows of another table
+    g = torch.Generator(device=DEV).manual_seed(1)
+    page = {}
+    for p in (8990, 8995):
+        for n in ("k", "v"):
+            cache[n][p] = torch.randint(0, 256, cache[n][p].shape, generator=g, device=DEV, dtype=torch.uint8)
+        for n in ("k_scale", "v_scale"):
+            cache[n][p] = torch.rand(Hkv, generator=g, device=DEV)
+        page[p] = {n: cache[n][p].clone() for n in ("k", "v", "k_scale", "v_scale")}
+
+    def holds(at, of):
+        return all(torch.equal(cache[n][at], page[of][n]) for n in page[of])
+
+    assert w4.kv8_fork(cache, refs, table, lens, ints([0, 0]), ints([1, 2])).tolist() == [0]
+    assert table.tolist() == [[8990, 8995], [8990, 0], [8990, 1]] and holds(0, 8995) and holds(1, 8995)
+    w4.kv8_free(refs, table, lens, ints([1]), T)
+    table, refs, used = w4.kv8_compact(cache, refs, table, lens)
+    assert used.tolist() == [8981] and table.tolist() == [[0, 8980], [-1, -1], [0, 1]]
+    assert holds(0, 8990) and holds(8980, 8995) and holds(1, 8995)
+    w4.kv8_copy_pages(cache, ints([8980]), ints([8999]))
+    assert holds(8999, 8995)

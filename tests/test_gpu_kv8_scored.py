@@ -36,7 +36,7 @@ def case(seed, lens, news, H, Hkv, D, T, dtype, size=1.0):
 
 
 def ints(v):
-    return torch.tensor(np.asarray(v).astype(np.int32), device=DEV)
+    return torch.tensor(np.asarray(v, np.int64).astype(np.int32), device=DEV)
 
 
 def call(c, fn=None, **more):
@@ -272,6 +272,41 @@ def test_refusals():
         w4.kv8_attention_scored(q, cache, table, lens, prefix=ints([0, 1, 2]))
     with pytest.raises(ValueError):
         w4.kv8_attention_scored(q[:, :, :32], cache, table, lens)
+    with pytest.raises(ValueError):
+        w4.kv8_attention_scored(q[0], cache, table, lens)
+    with pytest.raises(TypeError):
+        w4.kv8_attention_scored(q, cache, table, lens.tolist())
     none = q[:0]
     assert w4.kv8_attention_scored(none, cache, table[:0], lens[:0], softcap=3.0).shape == (0, 4, 64)
     assert math.isfinite(w4.kv8_attention_scored(q, cache, table, lens, softcap=None).float().sum().item())
+
+
+def test_workspace_of_both_attentions():
+    """One workspace for plain and scored calls in turn, split and not."""
+    space = None
+    for seed, (lens, news) in enumerate((([3000], [1]), ([2500, 100], [1, 1]), ([1500], [140]), ([2000], [3]))):
+        c = case(40 + seed, lens, news, 4, 1, 64, 32, "f16")
+        tokens = int(c["cu"][-1])
+        need = w4.kv8_attention_workspace_bytes(tokens, len(lens), max(news), max(lens), 4, 1, 64)
+        if space is None or space.numel() * 4 < need:
+            space = w4.workspace(max(need, 1 << 22), DEV)
+        slopes = torch.from_numpy(slopes_of(4).astype(np.float32)).to(DEV)
+        for _ in range(2):
+            a, _ = call(c, workspace=space, softcap=9.0, slopes=slopes)
+            p, _ = call(c, w4.kv8_attention, workspace=space)
+        assert torch.equal(a, call(c, softcap=9.0, slopes=slopes)[0])
+        assert torch.equal(p, call(c, w4.kv8_attention)[0])
+
+
+def test_two_streams_at_once():
+    c = case(50, [3000, 900], [1, 1], 8, 2, 128, 64, "bf16")
+    q, table, lens = c["q"], ints(c["table"]), ints(c["lens"])
+    want = [w4.kv8_attention_scored(q * (i + 1), c["cache"], table, lens, softcap=10.0 + i) for i in range(2)]
+    streams, xs = [torch.cuda.Stream() for _ in range(2)], [q * (i + 1) for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            got[i].append(w4.kv8_attention_scored(xs[i], c["cache"], table, lens, softcap=10.0 + i, stream=st))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])

@@ -169,3 +169,34 @@ def test_refusals():
         w4.w8a8_gated(x.cpu(), wq, ws)
     with pytest.raises(w4.W4A16Error, match="status 5"):
         w4.w8a8_gated(x.repeat(4, 1), wq, ws, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+def test_weights_at_two_gigabytes():
+    """The last rows of w below and beyond what one buffer holds, bit for bit as alone."""
+    K = 16384
+    w = torch.empty(2 * 65536, K, dtype=torch.int8, device=DEV)
+    for i in range(0, len(w), 8192):
+        w[i:i + 8192] = torch.randint(-127, 128, (8192, K), device=DEV, dtype=torch.int8)
+    ws = torch.rand(2 * 65536, device=DEV) * 1e-4
+    x = inputs(68, 1, 8, K, "bf16")[0]
+    for F in (65528, 65536):
+        say("gated, rows of w", 2 * F)
+        y = w4.w8a8_gated(x, w[:2 * F], ws[:2 * F])
+        for at in (0, F // 2 + 4, F - 8):
+            rows = [*range(at, at + 8), *range(F + at, F + at + 8)]
+            alone = w4.w8a8_gated(x, w[rows].contiguous(), ws[rows].contiguous())
+            assert torch.equal(y[:, at:at + 8], alone), (F, at)
+
+
+def test_two_streams_at_once():
+    """Each stream has a workspace of its own."""
+    cases = [inputs(70 + i, 100, 512, 1024, "f16") for i in range(2)]
+    want = [w4.w8a8_gated(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            got[i].append(w4.w8a8_gated(*cases[i], stream=st))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
