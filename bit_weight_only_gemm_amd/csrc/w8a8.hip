@@ -57,12 +57,14 @@ __device__ __forceinline__ u32x2_t codes8(const float (&f)[8], const Codes8& q) 
 template <int DT, int LANES>
 __global__ void __launch_bounds__(LANES)
 w8a8_quantize_kernel(const void* __restrict__ x, int64_t stride, int K, int8_t* __restrict__ codes,
-                     float* __restrict__ scales) {
+                     float* __restrict__ scales, uint32_t* __restrict__ counts, int num_counts) {
   constexpr int HOLD = kHeld / (8 * LANES), BYTES = DT == 2 ? 4 : 2, PARTS = BYTES / 2;
   __shared__ uint32_t part[LANES / 64];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
   const int64_t base = row * stride;
+  // counters of the product that follows, at zero
+  for (int i = (int)blockIdx.x * LANES + tid; i < num_counts; i += (int)gridDim.x * LANES) counts[i] = 0;
   // (a load past the row's end gives zeros)
   const rsrc_t r = make_rsrc((const uint8_t*)x + base * BYTES, (uint32_t)K * BYTES);
   u32x4_t raw[HOLD][PARTS];
@@ -123,20 +125,21 @@ w8a8_quantize_kernel(const void* __restrict__ x, int64_t stride, int K, int8_t* 
 
 template <int DT>
 void launch_quantize_dt(const void* x, int64_t M, int64_t K, int64_t stride, int8_t* codes,
-                        float* scales, hipStream_t st) {
+                        float* scales, uint32_t* counts, int num_counts, hipStream_t st) {
   if (M < kFewRows)
     hipLaunchKernelGGL((w8a8_quantize_kernel<DT, 1024>), dim3((unsigned)M), dim3(1024), 0, st, x,
-                       stride, (int)K, codes, scales);
+                       stride, (int)K, codes, scales, counts, num_counts);
   else
     hipLaunchKernelGGL((w8a8_quantize_kernel<DT, 256>), dim3((unsigned)M), dim3(256), 0, st, x,
-                       stride, (int)K, codes, scales);
+                       stride, (int)K, codes, scales, counts, num_counts);
 }
 
 hipError_t launch_quantize(const void* x, int64_t M, int64_t K, int64_t stride, int dtype,
-                           int8_t* codes, float* scales, hipStream_t st) {
+                           int8_t* codes, float* scales, hipStream_t st,
+                           uint32_t* counts = nullptr, int num_counts = 0) {
   (dtype == W4A16_F16    ? launch_quantize_dt<DT_F16>
    : dtype == W4A16_BF16 ? launch_quantize_dt<DT_BF16>
-                         : launch_quantize_dt<2>)(x, M, K, stride, codes, scales, st);
+                         : launch_quantize_dt<2>)(x, M, K, stride, codes, scales, counts, num_counts, st);
   return hipGetLastError();
 }
 
@@ -239,6 +242,23 @@ __device__ __forceinline__ void channels4(const float* sw, const uint16_t* bias,
   }
 }
 
+// K split over workgroups (gated tiles): partial sums in int32, [split][tile][BM BN],
+// and a counter for each tile, 0 before the call.  Sums of integers do not depend
+// on their order.
+struct Split {
+  int splits;
+  int32_t* parts;
+  uint32_t* count;
+};
+// Two sums past the caches of one die, for a workgroup on another.
+__device__ __forceinline__ void send2(int32_t* to, int a, int b) {
+  const uint64_t v = (uint64_t)(uint32_t)a | (uint64_t)(uint32_t)b << 32;
+  __hip_atomic_store((uint64_t*)to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t fetch2(const int32_t* from) {
+  return __hip_atomic_load((const uint64_t*)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Tile shape: WM x WN waves, each MT x NT products of 32 x 32.
 template <int MT_, int NT_, int WM_, int WN_, int NS_>
 struct Tile {
@@ -274,13 +294,16 @@ __global__ void __launch_bounds__(64 * TL::WAVES)
 w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
                  const int8_t* __restrict__ wq, const float* __restrict__ sw,
                  const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int M, int N,
-                 int K, int mb, int nb, int per_xcd, Gate gate) {
+                 int K, int mb, int nb, int per_xcd, Gate gate, Split sp) {
   constexpr int MT = TL::MT, NT = TL::NT, NS = TL::NS, L = TL::LOADS;
   __shared__ __attribute__((aligned(16))) uint8_t lds[NS * TL::STAGE];
   // ---- tile of this workgroup: workgroups go to the 8 XCDs in turn, so each
   // XCD takes a contiguous run of tiles, ordered in bands of 8 row blocks
-  const int at = (int)(blockIdx.x & 7) * per_xcd + (int)(blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per_xcd || at >= mb * nb) return;
+  // (gated: the splits of a tile follow one another)
+  const int splits = ACT ? sp.splits : 1;
+  const int turn = (int)(blockIdx.x >> 3) / splits, split = (int)(blockIdx.x >> 3) % splits;
+  const int at = (int)(blockIdx.x & 7) * per_xcd + turn;
+  if (turn >= per_xcd || at >= mb * nb) return;
   const int band = at / (8 * nb), in_band = at % (8 * nb);
   const int bh = min(8, mb - band * 8);
   const int row0 = (band * 8 + in_band % bh) * TL::BM, col0 = in_band / bh * TL::BN;
@@ -288,14 +311,18 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / TL::WN, wn = wave % TL::WN;
-  const int KT = (K + 127) >> 7;
+  // codes of this split, from the k0-th on (every split has some)
+  const int share = ACT ? (((K + 127) >> 7) + splits - 1) / splits * 128 : K;
+  const int k0 = ACT ? split * share : 0, KS = ACT ? min(share, K - k0) : K;
+  const int KT = (KS + 127) >> 7;
   // (gated: the waves being even in number, a wave's blocks are all of the gate's
   // rows or all of the up projection's)
   constexpr int HALVES = ACT ? 2 : 1;
   static_assert(TL::WAVES % 2 == 0, "blocks of w in turn");
-  const rsrc_t rw = make_rsrc(wq + (size_t)((ACT && (wave & 1) ? gate.F : 0) + col0 / HALVES) * K,
-                              (uint32_t)min(TL::BN, N - col0) / HALVES * (uint32_t)K);
-  const rsrc_t rx = make_rsrc(xq + (size_t)row0 * K, (uint32_t)min(TL::BM, M - row0) * (uint32_t)K);
+  const rsrc_t rw = make_rsrc(wq + (size_t)((ACT && (wave & 1) ? gate.F : 0) + col0 / HALVES) * K + k0,
+                              (uint32_t)min(TL::BN, N - col0) / HALVES * (uint32_t)K - (uint32_t)k0);
+  const rsrc_t rx = make_rsrc(xq + (size_t)row0 * K + k0,
+                              (uint32_t)min(TL::BM, M - row0) * (uint32_t)K - (uint32_t)k0);
 
   // load i of this wave fills the LDS block WAVES i + wave (8 rows); blocks
   // below BN / 8 are rows of w
@@ -307,7 +334,7 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
     const uint32_t chunk = ((uint32_t)lane & 7u) ^ ((row >> 1) & 7u);
     const uint32_t from = ACT && is_w ? 8u * (uint32_t)(blk >> 1) + (uint32_t)lrow : row;
     const uint32_t off =
-        128 * t + 16 * (int)chunk < K ? from * (uint32_t)K + 16u * chunk : kOutOfRange;
+        128 * t + 16 * (int)chunk < KS ? from * (uint32_t)K + 16u * chunk : kOutOfRange;
     dma16(is_w ? rw : rx, lds + (t % NS) * TL::STAGE + blk * 1024, off, t * 128);
   };
 
@@ -365,6 +392,46 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
   }
   // the loads past the last step have written their zeros
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // ---- splits: each leaves its sums and counts itself, the last to arrive adds
+  // them up.  They have gone past the die's cache before the count does.
+  if (ACT && splits > 1) {
+    constexpr int SUMS = TL::BM * TL::BN;
+    const int tiles = mb * nb, mine = wave * NT * MT * 1024 + lane * 4;
+    int32_t* part = sp.parts + ((size_t)split * tiles + at) * SUMS + mine;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          send2(part + ((i * MT + j) * 4 + (e >> 2)) * 256 + (e & 2), acc[i][j][e], acc[i][j][e + 1]);
+    // (in the ring, which is free: beside a second variable in LDS the compiler takes
+    // the loop's reads to wait for its loads, 0.6 us a step instead of 0.3)
+    uint32_t* arrived = (uint32_t*)lds;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0)
+      *arrived = __hip_atomic_fetch_add(sp.count + at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const bool last = *arrived == (uint32_t)splits - 1;
+    if (!last) return;
+    __syncthreads();  // the results go where it lies
+    for (int other = 0; other < splits; ++other) {
+      if (other == split) continue;
+      const int32_t* from = sp.parts + ((size_t)other * tiles + at) * SUMS + mine;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const uint64_t v = fetch2(from + ((i * MT + j) * 4 + (e >> 2)) * 256 + (e & 2));
+            acc[i][j][e] += (int)(uint32_t)v;
+            acc[i][j][e + 1] += (int)(uint32_t)(v >> 32);
+          }
+    }
+  }
 
   // ---- results: register i of product (nt, mt) is channel 8 (i >> 2) + 4 h +
   // (i & 3) of its 32, token lane & 31; one 32-token block of the wave at a time
@@ -992,15 +1059,17 @@ struct Args {
   uint16_t* out;
   int M, N, K;
   Gate gate;  // of the gated kernels
+  Split split;
 };
 
 template <int DT, class TL, int ACT>
 void launch_tile(const Args& a, hipStream_t st) {
   const int mb = (int)ceil_div(a.M, TL::BM), nb = (int)ceil_div(a.N, TL::BN);
   const int per_xcd = (int)ceil_div((int64_t)mb * nb, 8);
-  launch_timed(w8a8_tile_kernel<DT, TL, ACT>, dim3((unsigned)per_xcd * 8), dim3(64 * TL::WAVES), 0, st,
+  const unsigned splits = ACT ? (unsigned)a.split.splits : 1u;
+  launch_timed(w8a8_tile_kernel<DT, TL, ACT>, dim3(per_xcd * 8 * splits), dim3(64 * TL::WAVES), 0, st,
                (const int8_t*)a.x, a.sx, a.wq, a.sw, a.bias, a.out, a.M, a.N, a.K, mb, nb, per_xcd,
-               a.gate);
+               a.gate, a.split);
 }
 
 template <int DT, int MB, int NT, bool FUSED>
@@ -1041,34 +1110,23 @@ void launch_wide(const Args& a, hipStream_t st) {
 //   16 x 4096 x 11008 12.5 / 24.6, 16 x 8192 x 4096 11.2 / 11.8,
 //   16 x 12288 x 4096 14.7 / 12.0, 32 x 4096 x 4096 8.8 / 11.6,
 //   32 x 8192 x 4096 14.5 / 11.7, 64 x 4096 x 4096 12.5 / 12.0
-// The gated form has tiles of 192 x 256 too, 1.4 us a round (192 / 256 rows, M x F x
-// K): 333 x 13824 x 5120 72.9 / 81.7, 1024 x 11008 x 4096 130 / 119; (192 / 128 rows)
-// 192 x 13824 x 5120 64.2 / 64.9, 384 x 13824 x 5120 69 / 98.
-template <int DT, int ACT>
+template <int DT>
 hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
   const int64_t t64 = ceil_div(a.M, 64) * ceil_div(a.N, 64);
   const int64_t t128 = ceil_div(a.M, 128) * ceil_div(a.N, 128);
   const int64_t t256 = ceil_div(a.M, 256) * ceil_div(a.N, 256);
   const int64_t c64 = 3 * std::max<int64_t>(t64, 256), c128 = 6 * 256 * ceil_div(t128, 256),
                 c256 = 16 * 256 * ceil_div(t256, 256);
-  if constexpr (ACT != kNoGate) {
-    const int64_t t192 = ceil_div(a.M, 192) * ceil_div(a.N, 256);
-    const int64_t c192 = 14 * 256 * ceil_div(t192, 256);
-    if (c192 < c64 && c192 < c128 && c192 < c256) {
-      launch_wide<DT, ACT, 3>(a, st);
-      return hipGetLastError();
-    }
-  }
-  if (!ACT && a.M <= 64 && ceil_div(a.M, 16) * a.N < 12288) {
+  if (a.M <= 64 && ceil_div(a.M, 16) * a.N < 12288) {
     if (a.M > 32) launch_stream<DT, 4, 1, false>(a, st);
     else if (a.M > 16) launch_stream<DT, 2, 1, false>(a, st);
     else launch_stream<DT, 1, 1, false>(a, st);
   } else if (c64 <= c128 && c64 <= c256) {
-    launch_tile<DT, T64, ACT>(a, st);
+    launch_tile<DT, T64, kNoGate>(a, st);
   } else if (c128 <= c256) {
-    launch_tile<DT, T128, ACT>(a, st);
+    launch_tile<DT, T128, kNoGate>(a, st);
   } else {
-    launch_wide<DT, ACT, 4>(a, st);
+    launch_wide<DT, kNoGate, 4>(a, st);
   }
   return hipGetLastError();
 }
@@ -1076,8 +1134,8 @@ hipError_t launch_gemm_dt(const Args& a, hipStream_t st) {
 hipError_t launch_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                        const void* bias, void* out, int64_t M, int64_t N, int64_t K, int dtype,
                        hipStream_t st) {
-  const Args a = {xq, K, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K, {}};
-  return (dtype == DT_F16 ? launch_gemm_dt<DT_F16, kNoGate> : launch_gemm_dt<DT_BF16, kNoGate>)(a, st);
+  const Args a = {xq, K, sx, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M, (int)N, (int)K, {}, {}};
+  return (dtype == DT_F16 ? launch_gemm_dt<DT_F16> : launch_gemm_dt<DT_BF16>)(a, st);
 }
 
 // Channels per workgroup: 64 where that leaves two workgroups for each of 256
@@ -1093,7 +1151,7 @@ hipError_t launch_fused(const void* x, int64_t x_stride, const int8_t* wq, const
                         const void* bias, void* out, int64_t M, int64_t N, int64_t K, int dtype,
                         hipStream_t st) {
   const Args a = {x, x_stride, nullptr, wq, sw, (const uint16_t*)bias, (uint16_t*)out, (int)M,
-                  (int)N, (int)K, {}};
+                  (int)N, (int)K, {}, {}};
   (dtype == DT_F16 ? launch_fused_dt<DT_F16> : launch_fused_dt<DT_BF16>)(a, st);
   return hipGetLastError();
 }
@@ -1103,6 +1161,48 @@ bool few_gated(int64_t M, int64_t F, int64_t K) {
   return M <= 16 && M * K <= kCodes && 2 * F * K < ((int64_t)1 << 31);
 }
 bool fused_gated(int64_t M, int64_t F, int64_t K) { return few_gated(M, F, K) && M * K <= kFused; }
+
+// How the gated product of more tokens is formed: rows of a tile (64 x 64, 128 x
+// 128, 192 x 256 or 256 x 256), and workgroups that share a tile's K.
+//
+// The rule takes the least sum of us as measured on MI355X: a step of 128 codes of a
+// tile of 64 takes 0.3 (for at most one a CU, and in proportion beyond), of 128 0.45,
+// or 0.6 in each of several rounds, of 192 1.4 and of 256 1.6 a round; a join of s
+// splits 1 + 1.2 s and 4 + s.  Both sides (M x F x K, us, rows / splits):
+//   17 x 1696 x 13408 64/1 35.3, 64/4 19.4; 14 x 272 x 19680 64/1 47.6, 64/8 18.8;
+//   64 x 1376 x 4096 64/1 15.3, 64/3 12.4, 64/6 14.8; 128 x 2752 x 4096 64/1 15.6, 64/2
+//   16.5; 571 x 904 x 10592 64/1 52.1, 128/1 57.2, 128/3 39.0; 139 x 5192 x 16224 64/1
+//   95.6, 128/1 87.2; 333 x 13824 x 5120 128/1 96, 192 72.9, 256 81.7; 1024 x 11008 x
+//   4096 128/1 141, 192 130, 256 119
+struct GatedPlan {
+  int rows, splits;
+  int64_t tiles;
+};
+GatedPlan plan_gated(int64_t M, int64_t F, int64_t K) {
+  const int64_t N = 2 * F, KT = ceil_div(K, 128);
+  GatedPlan best = {0, 1, 0};
+  double least = 1e30;
+  auto offer = [&](int rows, int splits, int64_t tiles, double us) {
+    if (us < least) least = us, best = {rows, splits, tiles};
+  };
+  const int64_t t64 = ceil_div(M, 64) * ceil_div(N, 64), t128 = ceil_div(M, 128) * ceil_div(N, 128);
+  const int64_t t192 = ceil_div(M, 192) * ceil_div(N, 256), t256 = ceil_div(M, 256) * ceil_div(N, 256);
+  for (int s = 1; s <= 16 && (s == 1 || 4 * s <= KT); ++s) {
+    const double steps = (double)ceil_div(KT, s);
+    if (ceil_div(KT, ceil_div(KT, s)) != s) continue;  // a split would have none
+    if (s == 1 || t64 * s <= 512)
+      offer(64, s, t64, 0.3 * steps * std::max(1.0, t64 * s / 256.0) + (s > 1 ? 1 + 1.2 * s : 0));
+    if (s == 1 || t128 * s <= 256)
+      offer(128, s, t128, (t128 * s <= 256 ? 0.45 : 0.6 * ceil_div(t128 * s, 256)) * steps +
+                              (s > 1 ? 4 + s : 0));
+  }
+  offer(192, 1, t192, 1.4 * KT * ceil_div(t192, 256));
+  offer(256, 1, t256, 1.6 * KT * ceil_div(t256, 256));
+  return best;
+}
+int64_t split_bytes(const GatedPlan& p) {
+  return p.splits == 1 ? 0 : pad256(p.tiles * 4) + p.splits * p.tiles * p.rows * p.rows * 4;
+}
 
 template <int DT, int ACT, bool FUSED>
 void launch_gated_stream(const Args& a, hipStream_t st) {
@@ -1118,19 +1218,22 @@ void launch_gated_stream(const Args& a, hipStream_t st) {
                a.wq, a.sw, a.bias, a.out, a.M, a.K, tw, a.gate);
 }
 template <int DT, int ACT>
-hipError_t launch_gated_dt(const Args& a, hipStream_t st) {
+hipError_t launch_gated_dt(const Args& a, const GatedPlan& p, hipStream_t st) {
   if (!a.sx) launch_gated_stream<DT, ACT, true>(a, st);
   else if (few_gated(a.M, a.gate.F, a.K)) launch_gated_stream<DT, ACT, false>(a, st);
-  else return launch_gemm_dt<DT, ACT>(a, st);
+  else if (p.rows == 64) launch_tile<DT, T64, ACT>(a, st);
+  else if (p.rows == 128) launch_tile<DT, T128, ACT>(a, st);
+  else if (p.rows == 192) launch_wide<DT, ACT, 3>(a, st);
+  else launch_wide<DT, ACT, 4>(a, st);
   return hipGetLastError();
 }
 
 // A gated call on 16-bit rows (sx null) or on codes.
-hipError_t launch_gated(const Args& a, int act, int dtype, hipStream_t st) {
+hipError_t launch_gated(const Args& a, const GatedPlan& p, int act, int dtype, hipStream_t st) {
   if (act == W4A16_GELU)
-    return (dtype == DT_F16 ? launch_gated_dt<DT_F16, kErf> : launch_gated_dt<DT_BF16, kErf>)(a, st);
+    return (dtype == DT_F16 ? launch_gated_dt<DT_F16, kErf> : launch_gated_dt<DT_BF16, kErf>)(a, p, st);
   return (dtype == DT_F16 ? launch_gated_dt<DT_F16, kSigmoid>
-                          : launch_gated_dt<DT_BF16, kSigmoid>)(a, st);
+                          : launch_gated_dt<DT_BF16, kSigmoid>)(a, p, st);
 }
 
 // --------------------------------------------------------------- checking ---
@@ -1210,7 +1313,8 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
 
 int64_t w8a8_gated_workspace_bytes(int64_t M, int64_t F, int64_t K) {
   if (F <= 0 || F > kMaxN || F % 8 != 0 || validate_shape(M, 2 * F, K) != W4A16_OK) return -1;
-  return fused_gated(M, F, K) ? 0 : linear_bytes(M, K);
+  if (fused_gated(M, F, K)) return 0;
+  return linear_bytes(M, K) + (few_gated(M, F, K) ? 0 : split_bytes(plan_gated(M, F, K)));
 }
 
 int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w_scale,
@@ -1233,15 +1337,21 @@ int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w
     const float log2e = 1.4426950408889634f;
     const float a1 = act == W4A16_SILU ? log2e : 1.5957691216057308f * log2e;
     Args a = {x, x_stride, nullptr, wq, w_scale, (const uint16_t*)bias, (uint16_t*)out, (int)M,
-              (int)(2 * F), (int)K, {(int)F, a1, act == W4A16_SILU ? 0.0f : 0.044715f * a1}};
+              (int)(2 * F), (int)K, {(int)F, a1, act == W4A16_SILU ? 0.0f : 0.044715f * a1}, {1, nullptr, nullptr}};
+    GatedPlan p = {0, 1, 0};
     if (!fused_gated(M, F, K)) {
+      if (!few_gated(M, F, K)) p = plan_gated(M, F, K);
       int8_t* xq = (int8_t*)workspace;
       float* sx = (float*)(xq + pad256(M * K));
-      if (int s = hip_status(launch_quantize(x, M, K, x_stride, dtype, xq, sx, st))) return s;
+      uint32_t* count = (uint32_t*)(xq + linear_bytes(M, K));
+      if (int s = hip_status(launch_quantize(x, M, K, x_stride, dtype, xq, sx, st, count,
+                                             p.splits > 1 ? (int)p.tiles : 0)))
+        return s;
       a.x = xq;
       a.sx = sx;
+      a.split = {p.splits, (int32_t*)(count + pad256(p.tiles * 4) / 4), count};
     }
-    return hip_status(launch_gated(a, act, dtype, st));
+    return hip_status(launch_gated(a, p, act, dtype, st));
   });
 }
 

@@ -547,8 +547,8 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
  *        0.044715 g^3))).  Each within 2^-19 of itself and 2^-22 for each unit of
  *        the exponential's argument; below 2^-126 |g| it may be 0.
  * Constraints and limits as for w8a8_gemm with N = 2 F, F % 8 == 0; the
- * workspace (codes of x) as for w8a8_linear, by w8a8_gated_workspace_bytes (-1
- * on bad input).  Async.  Bitwise reproducible, and a row of y does not depend on
+ * workspace (codes of x, and sums where K is split over workgroups) as for
+ * w8a8_linear, by w8a8_gated_workspace_bytes (-1 on bad input).  Async.  Bitwise reproducible, and a row of y does not depend on
  * the other rows.
  */
 typedef enum { W4A16_SILU = 0, W4A16_GELU = 1, W4A16_GELU_TANH = 2 } w4a16_act_t;

@@ -38,9 +38,11 @@ SHAPES = [  # M, F, K
     (1, 264, 122880), (16, 24, 7680),                                                            # all of LDS
     (17, 72, 5136), (31, 2048, 512), (33, 136, 80), (64, 512, 4096), (16, 264, 7696), (1, 40, 122896),
     (100, 640, 1104), (129, 264, 5120), (255, 520, 1008),                                        # 64 x 64 tiles
+    (128, 2752, 272), (250, 11008, 80),
     (333, 1792, 1280), (1000, 1016, 688), (512, 2568, 512),                                      # 128 x 128
     (2049, 2312, 320), (2304, 2304, 16), (8192, 2304, 144),                                      # 256 x 256
     (333, 13832, 272), (1150, 4616, 144), (380, 27648, 64),                                      # 192 x 256
+    (17, 72, 13328), (14, 272, 19680), (65, 24, 4112), (200, 136, 8240), (300, 520, 12304),      # K split
 ]
 
 
@@ -200,3 +202,32 @@ def test_two_streams_at_once():
             got[i].append(w4.w8a8_gated(*cases[i], stream=st))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+
+
+@pytest.mark.parametrize("M,F,K", [(17, 72, 13328), (571, 904, 10592), (64, 1376, 4096)])
+def test_splits_of_k(M, F, K):
+    """Sums over split K are whole whatever the workspace held, on every call and
+    every replay, and the same bits as without a split (rows alone go through the
+    kernel for few tokens where they fit there)."""
+    x, wq, ws, b = inputs(80, M, F, K, "bf16")
+    need = w4.w8a8_gated_workspace_bytes(M, F, K)
+    assert need > w4.w8a8_workspace_bytes(M, 2 * F, K)
+    space = torch.full((need + 4096,), 255, dtype=torch.uint8, device=DEV)
+    y = w4.w8a8_gated(x, wq, ws, b, workspace=space[:need])
+    assert (space[need:] == 255).all()
+    for rows in (slice(0, 4), slice(M - 7, M)):
+        assert torch.equal(y[rows], w4.w8a8_gated(x[rows].contiguous(), wq, ws, b))
+    for _ in range(10):
+        space.random_(0, 256)
+        assert torch.equal(y, w4.w8a8_gated(x, wq, ws, b, workspace=space[:need]))
+    g, out = torch.cuda.CUDAGraph(), torch.empty_like(y)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        w4.w8a8_gated(x, wq, ws, b, out=out, workspace=space[:need])
+    for i in range(4):
+        x.copy_(torch.randn(M, K, generator=torch.Generator().manual_seed(i)))
+        want = w4.w8a8_gated(x, wq, ws, b)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
