@@ -150,16 +150,20 @@ __device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, i
   return row_limit(s, causal, min((rt * rows + rows - 1) / G, s.n - 1), prefix);
 }
 
-// Kernels are built for what they do to scores: kMasks nothing, else kCap and kBias.  (As branches at run time these cost the prompt kernel more registers
-// than it has: 30 ms instead of 1.6.)
+// Kernels are built for what they do to scores: kMasks nothing, else kCap and
+// kBias.  (As branches at run time these cost the prompt kernel more registers than
+// it has: 30 ms instead of 1.6.)
 //
 // tanh(x) = 1 - 2 / (1 + exp(2 x)), an exponential and a reciprocal of 1 ulp and
 // three roundings, is 2^-20 off at most, which the cap multiplies: 5e-5 of a
 // probability under a cap of 50, where its rounding to fp16 is 5e-4.  x P(x^2), P a
 // fit of degree 4 to tanh(x) / x over |x| < 3 / 4, is 9e-7 of itself off (2^-20) and
 // costs 28 cycles a wave and score instead of 44: a unit whose scores are all that
-// small under their cap takes it.  Under caps beyond kWideCap every small score does,
-// so that the error stays a part of the score.
+// small under their cap takes it (MI355X, chunks of 2048 over 8192, 40 / 8 heads,
+// under a cap of 50: 1383 us, 1559 with the exponential alone; without a cap 1112).
+// Under caps beyond kWideCap every small score does, so that the error stays a part
+// of the score.  (Keys that a row does not see count as 0 in this choice: what an
+// unused row of a page holds does not show in a result.)
 constexpr float kWideCap = 512.0f, kBend = 0.75f;
 
 __device__ __forceinline__ float tanh_near(float x) {
@@ -423,10 +427,18 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     const bool held = (whole || t0 + 16 * g < seq.len) &&
                       (!SCORED || t0 + (whole ? 63 : 16 * g + 15) >= low_min);
     float f = held ? f_row * ks : 0.0f;
+    // rows past the tile's last see what the others do; they are not written
+    const bool edge = t0 + kUnit > lim_all || (SCORED && t0 < low_max);
+    auto hidden = [&](int l) { return l >= lim || (SCORED && l < low); };
     if constexpr ((MODE & ~kMasks) != 0) {
       float t[1][16], factor[1] = {f};
 #pragma unroll
       for (int i = 0; i < 16; ++i) t[0][i] = s[i >> 2][i & 3];
+      if ((MODE & kCap) && edge) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (hidden(t0 + 16 * g + i)) t[0][i] = 0.0f;
+      }
       put_on<MODE>(t, factor, sc, slope, {(float)(seq.first + ridx / G - t0 - 16 * g)});
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] = t[0][i];
@@ -435,9 +447,6 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     if (f == 0.0f) f = 1e-37f;  // a hidden key stays at -inf
     const float v_scale = held ? vs : 0.0f;
     const float vs_top = whole ? v_scale : four_rows_max(v_scale);
-    // rows past the tile's last see what the others do; they are not written
-    const bool edge = t0 + kUnit > lim_all || (SCORED && t0 < low_max);
-    auto hidden = [&](int l) { return l >= lim || (SCORED && l < low); };
     if (edge) {
 #pragma unroll
       for (int a = 0; a < 4; ++a)
@@ -851,7 +860,9 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     if constexpr ((MODE & ~kMasks) != 0) {
       float t[2][16], factor[2] = {f[0], f[NSC - 1]};
 #pragma unroll
-      for (int i = 0; i < 32; ++i) t[i >> 4][i & 15] = s[i >> 4][i & 15];
+      for (int i = 0; i < 32; ++i)
+        t[i >> 4][i & 15] =
+            EDGE && (MODE & kCap) && hidden(t0 + 32 * (i >> 4) + 16 * h + (i & 15)) ? 0.0f : s[i >> 4][i & 15];
       const float back = (float)(position - t0 - 16 * h);
       put_on<MODE>(t, factor, sc, slope, {back, back - 32.0f});
 #pragma unroll

@@ -64,7 +64,8 @@ w8a8_quantize_kernel(const void* __restrict__ x, int64_t stride, int K, int8_t* 
   const int tid = threadIdx.x;
   const int64_t base = row * stride;
   // counters of the product that follows, at zero
-  for (int i = (int)blockIdx.x * LANES + tid; i < num_counts; i += (int)gridDim.x * LANES) counts[i] = 0;
+  for (int i = (int)blockIdx.x * LANES + tid; i < num_counts; i += (int)gridDim.x * LANES)
+    counts[i] = 0;
   // (a load past the row's end gives zeros)
   const rsrc_t r = make_rsrc((const uint8_t*)x + base * BYTES, (uint32_t)K * BYTES);
   u32x4_t raw[HOLD][PARTS];
@@ -139,7 +140,8 @@ hipError_t launch_quantize(const void* x, int64_t M, int64_t K, int64_t stride, 
                            uint32_t* counts = nullptr, int num_counts = 0) {
   (dtype == W4A16_F16    ? launch_quantize_dt<DT_F16>
    : dtype == W4A16_BF16 ? launch_quantize_dt<DT_BF16>
-                         : launch_quantize_dt<2>)(x, M, K, stride, codes, scales, counts, num_counts, st);
+                         : launch_quantize_dt<2>)(x, M, K, stride, codes, scales, counts,
+                                                  num_counts, st);
   return hipGetLastError();
 }
 
@@ -473,8 +475,8 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 }
 
 // The same product for many tokens: workgroups stay and take 64 MT x 256 tiles
-// in turn, 4 waves of 4 x MT products (MT = 4, and 3 in the gated form).  K goes by in steps of 128 codes (whole
-// 128-byte lines of w and x), four quarters of 32 each:
+// in turn, 4 waves of 4 x MT products (MT = 4, and 3 in the gated form).  K goes by
+// in steps of 128 codes (whole 128-byte lines of w and x), four quarters of 32 each:
 //
 //  * The rows of step t + 2 are loaded into registers while step t runs, each
 //    register right after its part of step t + 1 went from it to LDS, so a load
@@ -494,7 +496,9 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 // The matrix units bound it, at the clock the card holds under them: 8192 x
 // 55296 x 5120 in 1850 to 1950 us by card, 2.5 to 2.4 PFLOP/s, the units busy 68 %
 // of the cycles (2.57 with every load from L2, 2.82 without loads; with one tile
-// per workgroup and loads straight to LDS it took 2324 us).
+// per workgroup and loads straight to LDS it took 2324 us).  The gated form of it, 8192
+// x 27648 x 5120, takes 1926 us, its quantizing among them: half the results to write
+// pay for the activations.
 constexpr int kWideStage = 512 * 128, kWideTurn = 2 * kWideStage, kWideScales = kWideTurn + 4 * 4096;
 // x's scales, w's, the bias as fp32; of this tile and of the one before
 constexpr int kWideLds = kWideScales + 2 * 256 * 12;
@@ -887,6 +891,12 @@ w8a8_stream_kernel(const void* __restrict__ x, int64_t x_stride, const float* __
 //    places in turn, and before a wave writes into one it sees (without a wait,
 //    unless it is two groups ahead) that the group before there has been joined;
 //    whoever joins that one waits for nobody, so the wait ends.
+//
+// The stream of w bounds it (MI355X, whole calls, F x K): 1 token 28672 x 8192 80 us, 5.9
+// TB/s (95.7 in the form above, workgroups that end with their channels), 11008 x 4096
+// 19.9, 16 tokens of that 23.1 (29 in 64 x 64 tiles), 27648 x 5120 57, 5.0 TB/s.
+// With all 16 waves on one group and a barrier at its join it took 98 and 38 for the
+// first and the third: the joins held up the loads.
 constexpr int kCodes = 15 * 8192, kFused = 16384, kAhead = 4;
 
 template <int DT, int ACT, bool FUSED>

@@ -310,3 +310,22 @@ def test_two_streams_at_once():
             got[i].append(w4.kv8_attention_scored(xs[i], c["cache"], table, lens, softcap=10.0 + i, stream=st))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+
+
+@pytest.mark.parametrize("lens,news", [([201, 77], [1, 1]), ([201, 330], [140, 1])])
+def test_unused_rows_of_a_page_do_not_show(lens, news):
+    """Codes past a sequence's end, and before every query's first key, change no bit."""
+    for T in (16, 64):
+        c = case(60, lens, news, 4, 2, 64, T, "f16", size=0.5)
+        first = [70] * int(c["cu"][-1])
+        kw = dict(softcap=20.0, first=ints(first))
+        a, lse = call(c, **kw)
+        for b, L in enumerate(lens):
+            for p in range(-(-L // T)):
+                page = int(c["table"][b, p])
+                rows = [t for t in range(T) if not 70 <= p * T + t < L]
+                c["cache"]["k"][page][:, rows] = 255          # large scores, if they were seen
+                for t in rows:
+                    c["cache"]["v"][page][:, t // 16, :, t % 16] = 255
+        b, lse2 = call(c, **kw)
+        assert torch.equal(a, b) and torch.equal(lse, lse2)
