@@ -23,9 +23,9 @@ namespace w4a16 {
 // query sees:
 //   s <- cap tanh(s / cap) (cap > 0),  s <- s - slope[head] |position - l|,
 //   first[token] <= l < its limit, and below prefix[sequence] both ways.
-// Scores are in base 2 here (cap is times log2 e).  They are brought to their final
-// value before the maximum is taken, so that everything after it goes by them
-// with a factor of 1.
+// Scores are in base 2 here (cap is times log2 e).  They are brought to their
+// final value before the maximum is taken, but for the cap itself (or 1), by which
+// everything after it multiplies.
 struct Scoring {
   float cap, per_cap;     // and 1 / cap
   const float* slopes;    // [H] or null

@@ -64,7 +64,8 @@ def check(c, softcap=0.0, slopes=None, first=None, prefix=None):
     got = lse.double().cpu().numpy()
     assert np.array_equal(np.isneginf(got), np.isneginf(wlse))
     fine = np.isfinite(wlse)
-    assert np.all(np.abs(got - wlse)[fine] <= lb[fine]), np.max((np.abs(got - wlse) / lb)[fine])
+    err = np.abs(got[fine] - wlse[fine])
+    assert np.all(err <= lb[fine]), np.max(err / lb[fine])
     return o
 
 
