@@ -1341,6 +1341,9 @@ int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w
     if (!aligned16(bias) || !aligned16(workspace)) return W4A16_ERR_MISALIGNED;
     const int64_t need = w8a8_gated_workspace_bytes(M, F, K);
     if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+    // x is read while other workgroups write out
+    const int64_t from = (int64_t)(intptr_t)x, to = (int64_t)(intptr_t)out;
+    if (to < from + 2 * ((M - 1) * x_stride + K) && from < to + 2 * M * F) return W4A16_ERR_INVALID_ARG;
     clear_pending_error();
     const hipStream_t st = (hipStream_t)stream;
     // sigmoid(a g + b g^3): 1 and 0, or 2 sqrt(2 / pi) (1 and 0.044715); times log2 e

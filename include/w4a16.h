@@ -548,8 +548,9 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
  *        the exponential's argument; below 2^-126 |g| it may be 0.
  * Constraints and limits as for w8a8_gemm with N = 2 F, F % 8 == 0; the
  * workspace (codes of x, and sums where K is split over workgroups) as for
- * w8a8_linear, by w8a8_gated_workspace_bytes (-1 on bad input).  Async.  Bitwise reproducible, and a row of y does not depend on
- * the other rows.
+ * w8a8_linear, by w8a8_gated_workspace_bytes (-1 on bad input).  out must not
+ * lie between x's first and last value (W4A16_ERR_INVALID_ARG).  Async.
+ * Bitwise reproducible, and a row of y does not depend on the other rows.
  */
 typedef enum { W4A16_SILU = 0, W4A16_GELU = 1, W4A16_GELU_TANH = 2 } w4a16_act_t;
 int64_t w8a8_gated_workspace_bytes(int64_t M, int64_t F, int64_t K);
@@ -712,6 +713,10 @@ int kv8_attention_scored(const void* q, int64_t q_stride, const uint8_t* k_cache
  * the lowest on, in the order of the rows: results do not depend on timing.
  * Table entries out of [0, num_pages) are neither counted nor copied; a
  * length past the table's row counts as the whole row, one below 0 as 0.
+ * Lengths grow by kv8_reserve.  A caller that sets one back (to drop drafted
+ * tokens) must keep its count of pages, since pages past it are no longer known
+ * to be held, and may append again only if that last page's refs are 1: a page
+ * shared while it was whole would change for the other rows too.
  *   status     int32 [1], device, written by the call: 0 done; above 0 the
  *              pages that were missing; -1 refused rows.  Unless 0 the call
  *              has changed nothing else.

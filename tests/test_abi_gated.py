@@ -37,6 +37,13 @@ def test_refusals():
         assert call(**bad) == UNSUPPORTED, bad
 
 
+def test_out_over_x():
+    at = 0x100000
+    end = 2 * (63 * 80 + 64)       # bytes of x
+    for out in (at, at + 16, at + end - 16, at - 2 * 64 * 64 + 16):
+        assert call(x=ctypes.c_void_p(at), stride=80, out=ctypes.c_void_p(out)) == INVALID, out - at
+
+
 def test_workspace():
     need = L.w8a8_gated_workspace_bytes(64, 64, 64)
     assert need == 64 * 64 + 256 == L.w8a8_workspace_bytes(64, 128, 64, 1)       # codes and scales
