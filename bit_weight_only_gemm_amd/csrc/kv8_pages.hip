@@ -198,13 +198,13 @@ __global__ void __launch_bounds__(kPlan)
 kv8_reserve_kernel(Pool p, const int32_t* __restrict__ added, int32_t* __restrict__ status,
                    int32_t* __restrict__ ws) {
   __shared__ int part[kWaves];
-  __shared__ int long_row;
+  __shared__ int bad;  // a row that would be too long, or append to a page of others
   const int tid = threadIdx.x, lane = tid & 63;
-  if (tid == 0) long_row = 0;
+  if (tid == 0) bad = 0;
   __syncthreads();
   auto need_of = [&](int b, int& have, int64_t& len) {
     const int old = len_of(p, b);
-    len = (int64_t)old + max(added[b], 0);
+    len = max((int64_t)old + added[b], (int64_t)0);
     have = pages_of(p, old);
     return (int)min(((len + (1 << p.lgT) - 1) >> p.lgT) - have, (int64_t)p.width + 1);
   };
@@ -213,10 +213,14 @@ kv8_reserve_kernel(Pool p, const int32_t* __restrict__ added, int32_t* __restric
     const int b = at + tid;
     int need = 0, have;
     int64_t len = 0;
-    if (b < p.B) need = need_of(b, have, len);
+    if (b < p.B) need = max(need_of(b, have, len), 0);
     if (len > (int64_t)p.width << p.lgT) {
-      long_row = 1;
+      bad = 1;
       need = 0;
+    }
+    if (b < p.B && added[b] < 0 && (len & ((1 << p.lgT) - 1)) != 0) {
+      const int page = p.table[(int64_t)b * p.width + (len >> p.lgT)];
+      if (valid(p, page) && p.refs[page] > 1) bad = 1;
     }
     int total;
     const int first = before_me(need, part, total);
@@ -225,7 +229,7 @@ kv8_reserve_kernel(Pool p, const int32_t* __restrict__ added, int32_t* __restric
   }
   __syncthreads();
   int32_t* list = ws + p.B;
-  if (long_row) {
+  if (bad) {
     if (tid == 0) *status = -1;
     return;
   }
@@ -243,6 +247,11 @@ kv8_reserve_kernel(Pool p, const int32_t* __restrict__ added, int32_t* __restric
       const int page = list[ws[b] + i];
       p.table[(int64_t)b * p.width + have + i] = page;
       p.refs[page] = 1;
+    }
+    for (int i = need + lane; i < 0; i += 64) {  // given back: the row's last -need
+      int32_t* entry = p.table + (int64_t)b * p.width + have + i;
+      if (valid(p, *entry)) atomicSub(p.refs + *entry, 1);
+      *entry = -1;
     }
   }
   __syncthreads();  // the lengths have been read

@@ -713,10 +713,7 @@ int kv8_attention_scored(const void* q, int64_t q_stride, const uint8_t* k_cache
  * the lowest on, in the order of the rows: results do not depend on timing.
  * Table entries out of [0, num_pages) are neither counted nor copied; a
  * length past the table's row counts as the whole row, one below 0 as 0.
- * Lengths grow by kv8_reserve.  A caller that sets one back (to drop drafted
- * tokens) must keep its count of pages, since pages past it are no longer known
- * to be held, and may append again only if that last page's refs are 1: a page
- * shared while it was whole would change for the other rows too.
+ * Lengths grow and shrink by these calls alone.
  *   status     int32 [1], device, written by the call: 0 done; above 0 the
  *              pages that were missing; -1 refused rows.  Unless 0 the call
  *              has changed nothing else.
@@ -747,9 +744,12 @@ int kv8_free(int32_t* refs, int64_t num_pages, int32_t page_size, int32_t* page_
              void* stream);
 
 /*
- * Room for added[b] (int32 [B], device; below 0 as 0) more tokens in every row:
- * the pages they need are taken, and seq_lens become the lengths with them.
- * status -1: a row would pass max_pages * T.
+ * Room for added[b] (int32 [B], device) more tokens in every row: the pages they
+ * need are taken, and seq_lens become the lengths with them.  Below 0 that many
+ * last tokens are dropped (drafted ones; at most all), pages that this empties
+ * are given back, to be taken from the next call on, and their entries become -1.
+ * status -1: a row would pass max_pages * T, or end within a page that other
+ * rows hold too (which the next append would change for them).
  */
 int kv8_reserve(int32_t* refs, int64_t num_pages, int32_t page_size, int32_t* page_table,
                 int64_t max_pages, int32_t* seq_lens, int64_t B, const int32_t* added,

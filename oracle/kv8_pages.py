@@ -34,9 +34,13 @@ def reserve(pool, added):
     wants = []
     for b, n in enumerate(added):
         old = length(pool, b)
-        new = old + max(n, 0)
+        new = max(old + n, 0)
         if new > len(pool["table"][b]) * T:
             return -1, []
+        if n < 0 and new % T:
+            p = pool["table"][b][new // T]
+            if 0 <= p < len(pool["refs"]) and pool["refs"][p] > 1:
+                return -1, []
         wants += [(b, i) for i in range(-(-old // T), -(-new // T))]
     if len(wants) > len(free_pages):
         return len(wants) - len(free_pages), []
@@ -44,7 +48,12 @@ def reserve(pool, added):
         pool["table"][b][i] = p
         pool["refs"][p] = 1
     for b, n in enumerate(added):
-        pool["lens"][b] = length(pool, b) + max(n, 0)
+        old = length(pool, b)
+        pool["lens"][b] = max(old + n, 0)
+        for i in range(-(-pool["lens"][b] // T), -(-old // T)):
+            if 0 <= pool["table"][b][i] < len(pool["refs"]):
+                pool["refs"][pool["table"][b][i]] -= 1
+            pool["table"][b][i] = -1
     return 0, []
 
 

@@ -119,6 +119,8 @@ def test_oracle_reserve_takes_the_lowest_in_order_of_the_rows():
     p = pool([0, 1, 0, 0, 0], [[1, -1], [-1, -1], [-1, -1]], [16, 0, 0])
     assert oracle.reserve(p, [0, 17, 1]) == (0, [])
     assert p["table"] == [[1, -1], [0, 2], [3, -1]] and p["refs"] == [1, 1, 1, 1, 0] and p["lens"] == [16, 17, 1]
+    assert oracle.reserve({**p, "refs": [*p["refs"]], "lens": [*p["lens"]], "table": [[*t] for t in p["table"]]},
+                          [-1, 0, 0])[0] == 0
     assert oracle.reserve(p, [1, 0, 16]) == (1, []) and oracle.reserve(p, [17, 0, 0]) == (-1, [])
     assert p["lens"] == [16, 17, 1]
 

@@ -144,6 +144,35 @@ def test_reserve_refused_on_the_device(added, status):
     check(p, d, caches, want)
 
 
+DROPS = [([-1, -1, -1, 20, -1], 0), ([-40, -16, -7, 0, 0], 0), ([-2 ** 31, -1000, 5, -1, -2 ** 31], 0),
+         ([-33, 0, -8, 70, 1], 0),    # to the end of a page; all tokens; takes beside it
+         ([0, -3, 0, 200, 0], 1)]     # 13 pages, 12 free: nothing is dropped either
+
+
+@pytest.mark.parametrize("added,status", DROPS)
+def test_reserve_drops_tokens(added, status):
+    p, d, caches, want = make(14, [49, 16, 8, 0, 90], 16, 24, 16, stray=[(4, 5, -9)])
+    assert oracle.reserve(p, added)[0] == status
+    assert w4.kv8_reserve(d["refs"], d["table"], d["lens"], ints(added), 16).tolist() == [status]
+    check(p, d, caches, want)
+    more = [3, 30, 0, 1, 17]          # what was given back can be taken again
+    if status == 0:
+        assert oracle.reserve(p, more)[0] == 0
+        assert w4.kv8_reserve(d["refs"], d["table"], d["lens"], ints(more), 16).tolist() == [0]
+        check(p, d, caches, want)
+
+
+def test_reserve_does_not_end_rows_in_shared_pages():
+    for added, status in (([-1, 0, 0], 0), ([-10, 0, 0], -1), ([0, 0, -17], -1), ([-9, 0, -25], 0), ([-41, 0, 0], 0),
+                          ([1, 1, -9], 0)):
+        p, d, caches, want = make(15, [41, 7, 0], 4, 9, 16)
+        status_f, moves = oracle.fork(p, [0], [2])
+        assert w4.kv8_fork(caches, d["refs"], d["table"], d["lens"], ints([0]), ints([2])).tolist() == [status_f] == [0]
+        assert oracle.reserve(p, added)[0] == status
+        assert w4.kv8_reserve(d["refs"], d["table"], d["lens"], ints(added), 16).tolist() == [status]
+        check(p, d, caches, want, moves)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("shape", SHAPES)
 def test_compact(shape, in_place):
