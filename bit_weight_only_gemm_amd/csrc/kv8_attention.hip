@@ -10,8 +10,8 @@ namespace {
 // prompt kernel (MI355X, 24 sequences of 4001 tokens, 4 kv heads of 64: 40 rows
 // 28 us against 46 in the prompt kernel's form, 128 rows 45 against 53).
 // Splits of the keys: two workgroups for each of 256 CUs in all (64 sequences
-// of 8192 tokens, 8 kv heads of 128: 186 us; with 1024 workgroups 192, with
-// 3072 215), no split below 8 units, two a wave (with 4, one sequence of 777
+// of 8192 tokens, 8 kv heads of 128: 186 us; with 1024 workgroups 192, with thrice
+// those 215), no split below 8 units, two a wave (with 4, one sequence of 777
 // tokens and 32 kv heads takes 8.7 us instead of 9.7, but 8 of 2000 and 8 kv heads
 // 12.6 instead of 11.1 and one of 20000 26.5 instead of 20.1: the join grows with
 // the splits); the prompt kernel's 4.
