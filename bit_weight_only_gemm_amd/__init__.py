@@ -53,6 +53,19 @@ def _need(t, dtype, name, numel=None):
         raise ValueError("%s has %d elements, expected %d" % (name, t.numel(), numel))
 
 
+def _space_bytes(workspace, device):
+    """Bytes of a workspace (None: 0) that the kernels on `device` write over."""
+    if workspace is None:
+        return 0
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
+        raise TypeError("workspace must be a CUDA (HIP) tensor")
+    if workspace.device != device:
+        raise ValueError("workspace is on %s, the call's tensors on %s" % (workspace.device, device))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _here(stream, *tensors):
     """Refuses tensors (None: an argument not given) and a stream of another
     device than the current one, on which the kernels are launched."""
@@ -232,7 +245,7 @@ def _int4_gemm(x, x_scale, packed, out, workspace, use_workspace, stream):
         need = w4a16_workspace_bytes(M, N, K, G)
         if workspace is None and need > 0:
             workspace = _ws_cache(x.device, need, stream)
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        ws_bytes = _space_bytes(workspace, x.device)
     else:
         workspace = None
     L = _lib.lib()
@@ -354,7 +367,7 @@ def nf4_gemm(x, nf4, out=None, workspace=None, use_workspace=True, stream=None):
         need = nf4_workspace_bytes(M, N, K, bs)
         if workspace is None and need > 0:
             workspace = _ws_cache(x.device, need, stream)
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        ws_bytes = _space_bytes(workspace, x.device)
     else:
         workspace = None
     rp = "qweight_r" in nf4

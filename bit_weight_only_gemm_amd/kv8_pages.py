@@ -120,7 +120,7 @@ def kv8_reserve(refs, page_table, seq_lens, added, page_size, status=None, works
     _need(refs, torch.int32, "refs")
     B, width = _rows(page_table, seq_lens)
     _need(added, torch.int32, "added", B)
-    _here(stream, refs, page_table, seq_lens, added, status)
+    _here(stream, refs, page_table, seq_lens, added, status, workspace)
     status = _status(status, refs, stream)
     workspace, nbytes = _space(workspace, kv8_pages_workspace_bytes(refs.numel(), B), refs.device,
                                stream)
@@ -142,7 +142,7 @@ def kv8_fork(caches, refs, page_table, seq_lens, src, dst, status=None, workspac
     _need(src, torch.int32, "src")
     n = src.numel()
     _need(dst, torch.int32, "dst", n)
-    _here(stream, refs, page_table, seq_lens, src, dst, status, *_arrays(caches))
+    _here(stream, refs, page_table, seq_lens, src, dst, status, workspace, *_arrays(caches))
     status = _status(status, refs, stream)
     workspace, nbytes = _space(workspace, kv8_pages_workspace_bytes(pages, B, n), refs.device,
                                stream)
@@ -162,7 +162,8 @@ def kv8_compact(caches, refs, page_table, seq_lens, page_table_out=None, refs_ou
     still goes by the old table stays right until they are taken again."""
     arrays, count, pages, T, Hkv, D = _caches(caches, refs)
     B, width = _rows(page_table, seq_lens)
-    _here(stream, refs, page_table, seq_lens, page_table_out, refs_out, *_arrays(caches))
+    _here(stream, refs, page_table, seq_lens, page_table_out, refs_out, workspace,
+          *_arrays(caches))
     device = refs.device
     if page_table_out is None:
         page_table_out = _empty((B, width), torch.int32, device, stream)

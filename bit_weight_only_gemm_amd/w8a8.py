@@ -14,7 +14,7 @@ or, for rows quantized once and used by several layers:
 
 import torch
 
-from . import _DT, _here, _lib, _need, _stream, _ws_cache
+from . import _DT, _here, _lib, _need, _space_bytes, _stream, _ws_cache
 
 _QDT = dict(_DT)
 _QDT[torch.float32] = 2
@@ -105,8 +105,7 @@ def _output(out, shape, dtype, device, stream):
 def _space(workspace, need, device, stream, kept=None):
     if workspace is None and need > 0:
         workspace = _ws_cache(device, need, stream, kept)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return workspace, nbytes
+    return workspace, _space_bytes(workspace, device)
 
 
 def w8a8_gemm(xq, x_scale, wq, w_scale, bias=None, dtype=torch.bfloat16, out=None,
