@@ -390,8 +390,11 @@ def nf4_dequant(nf4, dtype=torch.bfloat16, stream=None):
 
 # One workspace per (device, stream), grown on demand and reused by later
 # calls on that stream (calls on one stream run in order; the kernels write
-# every workspace byte they read, so its contents do not matter).
+# every workspace byte they read, so its contents do not matter).  One that is
+# outgrown keeps its memory, since a graph captured on the stream goes on writing
+# there; sizes at least double, so that all of these are less than the last.
 _WS = {}
+_OUTGROWN = []
 
 
 def _ws_cache(device, nbytes, stream=None, kept=None):
@@ -401,6 +404,9 @@ def _ws_cache(device, nbytes, stream=None, kept=None):
     if cur is None or cur.numel() * 4 < nbytes:
         st = torch.cuda.current_stream() if stream is None else stream
         st.synchronize()
+        if cur is not None:
+            _OUTGROWN.append(cur)
+            nbytes = max(nbytes, 8 * cur.numel())
         with torch.cuda.stream(st):     # a block of the stream that uses it
             cur = workspace(max(nbytes, 1 << 20), device)
         kept[key] = cur
