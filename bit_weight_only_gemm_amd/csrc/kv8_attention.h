@@ -157,7 +157,7 @@ __device__ __forceinline__ int tile_limit(const Kv8Seq& s, int causal, int rt, i
 // tanh(x) = 1 - 2 / (1 + exp(2 x)), an exponential and a reciprocal of 1 ulp and
 // three roundings, is 2^-20 off at most, which the cap multiplies: 5e-5 of a
 // probability under a cap of 50, where its rounding to fp16 is 5e-4.  x P(x^2), P a
-// fit of degree 4 to tanh(x) / x over |x| < 3 / 4, is 9e-7 of itself off (2^-20) and
+// fit of degree 4 to tanh(x) / x over |x| < 3 / 4, is 9.1e-7 of itself off (2^-20) and
 // costs 28 cycles a wave and score instead of 44: a unit whose scores are all that
 // small under their cap takes it (MI355X, chunks of 2048 over 8192, 40 / 8 heads,
 // under a cap of 50: 1383 us, 1559 with the exponential alone; without a cap 1112).

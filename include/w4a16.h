@@ -683,7 +683,7 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
  * Visible are max(first, 0) <= l < e, e = max(p + 1, prefix) when causal (0 for a
  * negative p), and at most seq_lens[b]; keys before every query's `first` are not
  * read.  A query that sees nothing gives 0 (and lse -inf).  Scores are fp32 in
- * all of this; the cap is off by 2^-22 softcap up to 350, by 2^-20 of the score
+ * all of this; the cap is off by 2^-20 softcap up to 350, by 2^-19 of the score
  * beyond.  Arguments, workspace (kv8_attention_workspace_bytes; it may be
  * kv8_attention's) and errors otherwise as for kv8_attention.  Async.  Bitwise
  * reproducible.
