@@ -70,6 +70,10 @@ SIGNATURES = {
                                         _c.c_float, _i32, _c.c_float, _p, _p, _p, _p, _i64, _p,
                                         _i64, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _p, _i64,
                                         _p]),
+    "kv8_attention_scored_ends": (_c.c_int, [_p, _i64, _p, _p, _p, _p, _i64, _i32, _p, _i64, _p, _p,
+                                             _c.c_float, _i32, _c.c_float, _p, _p, _p, _p, _p,
+                                             _i64, _p, _i64, _i64, _i64, _i64, _i32, _i32, _i32,
+                                             _i32, _p, _i64, _p]),
     "kv8_pages_workspace_bytes": (_i64, [_i64, _i64, _i64]),
     "kv8_copy_pages": (_c.c_int, [_p, _i32, _i64, _i32, _i32, _i32, _p, _p, _i64, _p]),
     "kv8_free": (_c.c_int, [_p, _i64, _i32, _p, _i64, _p, _i64, _p, _i64, _p]),

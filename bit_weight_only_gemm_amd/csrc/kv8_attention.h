@@ -22,7 +22,8 @@ namespace w4a16 {
 // What the scored form puts on the scores before the softmax, and which keys a
 // query sees:
 //   s <- cap tanh(s / cap) (cap > 0),  s <- s - slope[head] |position - l|,
-//   first[token] <= l < its limit, and below prefix[sequence] both ways.
+//   first[token] <= l < its limit, and below prefix[sequence] both ways; but
+//   never from end[token] on.
 // Scores are in base 2 here (cap is times log2 e).  They are brought to their
 // final value before the maximum is taken, but for the cap itself (or 1), by which
 // everything after it multiplies.
@@ -31,6 +32,7 @@ struct Scoring {
   const float* slopes;    // [H] or null
   const int32_t* first;   // [tokens] or null
   const int32_t* prefix;  // [B] or null
+  const int32_t* end;     // [tokens] or null
 };
 
 // What a kernel is built to do to scores.
@@ -317,7 +319,26 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const bool rv = ridx < seq.n * G;
   const int tok = seq.tok + (rv ? ridx / G : 0), head = hk * G + (rv ? ridx % G : 0);
   const int prefix = SCORED && sc.prefix ? sc.prefix[b] : 0;
-  const int lim = rv ? row_limit(seq, causal, ridx / G, prefix) : 0;
+  int lim = rv ? row_limit(seq, causal, ridx / G, prefix) : 0;
+  // rows with ends: the largest limit, the least, and where tokens begin that hold
+  // nothing which some row sees
+  int lim_most = 0, lim_least = 0, held_to = seq.len;
+  if (SCORED && sc.end) {
+    const int end = rv ? clamp_int(sc.end[tok], 0, seq.len) : 0;
+    lim = min(lim, end);
+    lim_most = lim;
+    lim_least = rv ? lim : INT32_MAX;
+    held_to = end;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      lim_most = max(lim_most, __shfl_xor(lim_most, o, 64));
+      lim_least = min(lim_least, __shfl_xor(lim_least, o, 64));
+      held_to = max(held_to, __shfl_xor(held_to, o, 64));
+    }
+    lim_most = __builtin_amdgcn_readfirstlane(lim_most);
+    lim_least = __builtin_amdgcn_readfirstlane(lim_least);
+    held_to = __builtin_amdgcn_readfirstlane(held_to);
+  }
   // first key that this row sees, that some row and that every row does
   int low = 0, low_min = 0, low_max = 0;
   if (SCORED && sc.first) {
@@ -335,7 +356,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const float slope = (MODE & kBias) != 0 ? sc.slopes[head] * kLog2e : 0.0f;
 
   // units nu0 .. nu - 1, this split's u0 .. u1 - 1
-  const int top = tile_limit(seq, causal, rt, 16, G, prefix);
+  const int top = SCORED && sc.end ? lim_most : tile_limit(seq, causal, rt, 16, G, prefix);
   const int nu = (top + kUnit - 1) / kUnit, nu0 = min(low_min / kUnit, nu);
   const int share = split_units(nu - nu0, splits, units);
   const int u0 = nu0 + split * share, u1 = min(u0 + share, nu);
@@ -405,7 +426,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     turn_pages(u0 + wave + 4);
   }
   // keys that every row of the tile sees
-  const int lim_all = row_limit(seq, causal, rt * 16 / G, prefix);
+  const int lim_all = SCORED && sc.end ? lim_least : row_limit(seq, causal, rt * 16 / G, prefix);
   const bool whole = c.lgT >= 6;  // a unit lies in one page
   for (int u = u0 + wave; u < u1; u += 4) {
     const int t0 = u * kUnit;
@@ -424,7 +445,7 @@ kv8_decode_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
     __builtin_amdgcn_sched_barrier(0);
     // past the sequence's end it may be no page of this sequence
     // (scored: nor does the scale matter of tokens that no row sees)
-    const bool held = (whole || t0 + 16 * g < seq.len) &&
+    const bool held = (whole || t0 + 16 * g < held_to) &&
                       (!SCORED || t0 + (whole ? 63 : 16 * g + 15) >= low_min);
     float f = held ? f_row * ks : 0.0f;
     // rows past the tile's last see what the others do; they are not written
@@ -689,14 +710,36 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const bool rv = ridx < seq.n * G;
   const int tok = seq.tok + (rv ? ridx / G : 0), head = hk * G + (rv ? ridx % G : 0);
   const int prefix = SCORED && sc.prefix ? sc.prefix[b] : 0;
-  const int lim = rv ? row_limit(seq, causal, ridx / G, prefix) : 0;
+  int lim = rv ? row_limit(seq, causal, ridx / G, prefix) : 0;
   // keys that every row of this wave sees
-  const int lim_all = row0 + 31 < seq.n * G ? row_limit(seq, causal, row0 / G, prefix) : 0;
+  int lim_all = row0 + 31 < seq.n * G ? row_limit(seq, causal, row0 / G, prefix) : 0;
+  // rows with ends: the largest limit of the workgroup; and where tokens begin that
+  // hold nothing which some row of this wave sees
+  int lim_most = 0, held_to = WHOLE ? INT32_MAX : seq.len;
   // first key that this row sees, that some row of the workgroup and that every
   // row of this wave does
   int low = 0, low_min = 0, low_max = 0, low_wave = 0;
   if constexpr (SCORED) {
-    __shared__ int lows[W];
+    __shared__ int lows[W], tops[W];
+    if (sc.end) {
+      const int end = rv ? clamp_int(sc.end[tok], 0, seq.len) : 0;
+      lim = min(lim, end);
+      lim_most = lim_all = lim;
+      held_to = end;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        lim_most = max(lim_most, __shfl_xor(lim_most, o, 64));
+        lim_all = min(lim_all, __shfl_xor(lim_all, o, 64));
+        held_to = max(held_to, __shfl_xor(held_to, o, 64));
+      }
+      lim_all = __builtin_amdgcn_readfirstlane(lim_all);
+      held_to = __builtin_amdgcn_readfirstlane(held_to);
+      if (lane == 0) tops[wave] = lim_most;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) lim_most = max(lim_most, tops[w]);
+      lim_most = __builtin_amdgcn_readfirstlane(lim_most);
+    }
     if (sc.first) {
       low = rv ? max(sc.first[tok], 0) : 0;
       low_max = low;
@@ -720,7 +763,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
   const int position = seq.first + ridx / G;
 
   // units nu0 .. nu - 1, this split's u0 .. u1 - 1
-  const int top = tile_limit(seq, causal, rt, ROWS, G, prefix);
+  const int top = SCORED && sc.end ? lim_most : tile_limit(seq, causal, rt, ROWS, G, prefix);
   const int nu = (top + kUnit - 1) / kUnit, nu0 = min(low_min / kUnit, nu);
   const int share = split_units(nu - nu0, splits, units);
   const int u0 = nu0 + split * share, u1 = min(u0 + share, nu);
@@ -851,7 +894,7 @@ kv8_prompt_kernel(Kv8 c, const uint16_t* __restrict__ q, int64_t q_stride, float
       asm volatile("" : "+v"(ks_next[a]), "+v"(vs_next[a]));
       // past the sequence's end it may be no page of this sequence
       // (scored: nor does the scale matter of tokens that no row of the wave sees)
-      const bool held = (WHOLE || t0 + 32 * a + 16 * h < seq.len) &&
+      const bool held = ((WHOLE && !SCORED) || t0 + (WHOLE ? 0 : 32 * a + 16 * h) < held_to) &&
                         (!SCORED || t0 + (WHOLE ? 63 : 32 * a + 16 * h + 15) >= low_wave);
       f[a] = held ? f_row * ks_next[a] : 0.0f;
       vs[a] = held ? vs_next[a] : 0.0f;

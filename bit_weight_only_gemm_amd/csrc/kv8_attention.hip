@@ -57,7 +57,8 @@ int attention(int mode, const void* q, int64_t q_stride, const uint8_t* k_cache,
     if (int s = check_ptrs({q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out}))
       return s;
     for (const void* p : {(const void*)cu_seqlens, (const void*)lse, (const void*)workspace,
-                          (const void*)sc.slopes, (const void*)sc.first, (const void*)sc.prefix})
+                          (const void*)sc.slopes, (const void*)sc.first, (const void*)sc.prefix,
+                          (const void*)sc.end})
       if (!aligned16(p)) return W4A16_ERR_MISALIGNED;
     const Plan p = plan_attention(B, max_new, max_len, H, Hkv, D);
     const int64_t need = part_bytes(p, tokens, H, D);
@@ -116,10 +117,28 @@ int kv8_attention_scored(const void* q, int64_t q_stride, const uint8_t* k_cache
                          int64_t out_stride, float* lse, int64_t tokens, int64_t B,
                          int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
                          int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  return kv8_attention_scored_ends(q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages,
+                                   page_size, page_table, max_pages, seq_lens, cu_seqlens, scale,
+                                   causal, softcap, slopes, first, nullptr, prefix, out,
+                                   out_stride, lse, tokens, B, max_new, max_len, H, Hkv, D, dtype,
+                                   workspace, workspace_bytes, stream);
+}
+
+int kv8_attention_scored_ends(const void* q, int64_t q_stride, const uint8_t* k_cache,
+                              const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                              int64_t num_pages, int32_t page_size, const int32_t* page_table,
+                              int64_t max_pages, const int32_t* seq_lens,
+                              const int32_t* cu_seqlens, float scale, int32_t causal,
+                              float softcap, const float* slopes, const int32_t* first,
+                              const int32_t* end, const int32_t* prefix, void* out,
+                              int64_t out_stride, float* lse, int64_t tokens, int64_t B,
+                              int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
+                              int32_t dtype, void* workspace, int64_t workspace_bytes,
+                              void* stream) {
   // (beyond these the quotients of scores and cap leave fp32)
   if (softcap != 0.0f && !(softcap >= 1e-3f && softcap <= 1e30f)) return W4A16_ERR_INVALID_ARG;
   const float cap = softcap * kLog2e;
-  const Scoring sc = {cap, 1.0f / cap, slopes, first, prefix};
+  const Scoring sc = {cap, 1.0f / cap, slopes, first, prefix, end};
   const int mode = kMasks | (softcap == 0.0f ? 0 : kCap) | (slopes ? kBias : 0);
   return attention(mode, q, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
                          page_table, max_pages, seq_lens, cu_seqlens, scale, causal, sc, out,

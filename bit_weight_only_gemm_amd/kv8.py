@@ -173,27 +173,37 @@ def kv8_attention(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
 
 def kv8_attention_scored(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
                          max_len=None, scale=None, causal=True, softcap=0.0, slopes=None,
-                         first=None, prefix=None, out=None, lse=None, workspace=None, stream=None):
+                         first=None, prefix=None, out=None, lse=None, workspace=None, stream=None,
+                         end=None):
     """kv8_attention of scores s = scale q . k that become softcap tanh(s /
     softcap) (0 or None: as they are), less slopes[h] |distance| (fp32 [H]).
     first (int32 [tokens]): the first position that each query sees, the start of
     its document or of a window.  prefix (int32 [B]): with causal, positions below
-    it are seen by every query of the sequence.  A query that sees nothing gives 0.
-    The other arguments as for kv8_attention, its workspace among them."""
+    it are seen by every query of the sequence.  end (int32 [tokens]): no query
+    sees this position or those after it; documents that share a sequence need it
+    beside first where they are seen both ways (causal=False, or a prefix, which
+    reaches into the documents after a query's own).  A query that sees nothing
+    gives 0.  The other arguments as for kv8_attention, its workspace among them."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [tokens, heads, D]")
     _need(seq_lens, torch.int32, "seq_lens")
-    extra = [0.0 if softcap is None else float(softcap), None, None, None]
+    extra = [0.0 if softcap is None else float(softcap), None, None, None, None]
     for i, (t, dtype, name, n) in enumerate(((slopes, torch.float32, "slopes", q.shape[1]),
                                              (first, torch.int32, "first", q.shape[0]),
+                                             (end, torch.int32, "end", q.shape[0]),
                                              (prefix, torch.int32, "prefix", seq_lens.numel()))):
         if t is not None:
             _need(t, dtype, name, n)
             extra[1 + i] = t.data_ptr()
-    _here(stream, q, cache["k"], page_table, seq_lens, cu_seqlens, slopes, first, prefix, out, lse,
-          workspace)
-    return _attention("kv8_attention_scored", extra, q, cache, page_table, seq_lens, cu_seqlens,
-                      max_new, max_len, scale, causal, out, lse, workspace, stream)
+    _here(stream, q, cache["k"], page_table, seq_lens, cu_seqlens, slopes, first, end, prefix, out,
+          lse, workspace)
+    name = "kv8_attention_scored"
+    if end is None:
+        del extra[3]
+    else:
+        name += "_ends"
+    return _attention(name, extra, q, cache, page_table, seq_lens, cu_seqlens, max_new, max_len,
+                      scale, causal, out, lse, workspace, stream)
 
 
 def _attention(name, extra, q, cache, page_table, seq_lens, cu_seqlens, max_new, max_len, scale,

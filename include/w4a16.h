@@ -671,18 +671,26 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
 
 /*
  * kv8_attention of scores that are capped, or get a bias by distance, and under
- * masks of documents and prefixes:
+ * masks of documents, windows and prefixes:
  *   s = scale q . K[l],  s <- softcap tanh(s / softcap),
  *   s <- s - slopes[h] |p - l|,  p the query's position, and then as above.
  *   softcap  0: none; else 1e-3 to 1e30 (W4A16_ERR_INVALID_ARG).
  *   slopes   fp32 [H] or NULL: none.
  *   first    int32 [tokens] or NULL (0): a query sees no key before this one, so
  *            the start of its document, or of a window.
+ *   end      int32 [tokens] or NULL (none): nor this one and those after it, so
+ *            the end of its document.  (kv8_attention_scored_ends; without a
+ *            prefix a causal query's own position ends what it sees of its
+ *            document, and `first` is enough.)
  *   prefix   int32 [B] or NULL (0): with causal, every query of the sequence also
- *            sees the cached tokens below it, those after it among them.
+ *            sees the cached tokens below it, those after it among them: those of
+ *            later documents too, unless `end` keeps them out.
  * Visible are max(first, 0) <= l < e, e = max(p + 1, prefix) when causal (0 for a
- * negative p), and at most seq_lens[b]; keys before every query's `first` are not
- * read.  A query that sees nothing gives 0 (and lse -inf).  Scores are fp32 in
+ * negative p), else seq_lens[b], and at most end and seq_lens[b]; keys before every
+ * query's `first`, or from every query's `end` on, are not read.  So several
+ * documents in one sequence are kept apart by `first` when causal, and by `first`
+ * and `end` where they are seen both ways: all of each (causal 0), or up to the
+ * prefix.  A query that sees nothing gives 0 (and lse -inf).  Scores are fp32 in
  * all of this; the cap is off by 2^-20 softcap up to 350, by 2^-19 of the score
  * beyond.  Arguments, workspace (kv8_attention_workspace_bytes; it may be
  * kv8_attention's) and errors otherwise as for kv8_attention.  Async.  Bitwise
@@ -697,6 +705,17 @@ int kv8_attention_scored(const void* q, int64_t q_stride, const uint8_t* k_cache
                          int64_t out_stride, float* lse, int64_t tokens, int64_t B,
                          int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
                          int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream);
+int kv8_attention_scored_ends(const void* q, int64_t q_stride, const uint8_t* k_cache,
+                              const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                              int64_t num_pages, int32_t page_size, const int32_t* page_table,
+                              int64_t max_pages, const int32_t* seq_lens,
+                              const int32_t* cu_seqlens, float scale, int32_t causal,
+                              float softcap, const float* slopes, const int32_t* first,
+                              const int32_t* end, const int32_t* prefix, void* out,
+                              int64_t out_stride, float* lse, int64_t tokens, int64_t B,
+                              int64_t max_new, int64_t max_len, int32_t H, int32_t Hkv, int32_t D,
+                              int32_t dtype, void* workspace, int64_t workspace_bytes,
+                              void* stream);
 
 /* ------------------------------------------------- pages of the 8-bit cache --- */
 

@@ -94,7 +94,7 @@ def attention_bounds(out, mass, work, tokens_seen, D, dtype):
 
 
 def attention_scored(q, k, v, table, lens, cu, T, scale, causal, softcap=0.0, slopes=None, first=None, prefix=None,
-                     scale_ratio=1.0):
+                     scale_ratio=1.0, end=None):
     """attention() of capped and biased scores under document and prefix masks:
     (out, lse, bound of |out - exact| before its last rounding, bound of |lse -
     exact|).
@@ -126,6 +126,7 @@ def attention_scored(q, k, v, table, lens, cu, T, scale, causal, softcap=0.0, sl
         for j in range(n):
             t, p = cu[b] + j, lens[b] - n + j
             hi = min(lens[b], (max(p + 1, prefix[b] if prefix is not None else 0) if p >= 0 else 0) if causal else lens[b])
+            hi = hi if end is None else min(hi, end[t])
             lo = max(first[t], 0) if first is not None else 0
             if lo >= hi:
                 continue
