@@ -281,7 +281,7 @@ kv8_fork_plan_kernel(Pool p, const int32_t* __restrict__ src, const int32_t* __r
   __syncthreads();
   for (int i = tid; i < n; i += kPlan) {
     const int s = src[i], d = dst[i];
-    if ((uint32_t)s >= (uint32_t)p.B || (uint32_t)d >= (uint32_t)p.B || p.lens[d] != 0) bad = 1;
+    if ((uint32_t)s >= (uint32_t)p.B || (uint32_t)d >= (uint32_t)p.B || p.lens[d] > 0) bad = 1;
     else marks[s] = marks[d] = 0;
   }
   __syncthreads();

@@ -60,7 +60,7 @@ def reserve(pool, added):
 def fork(pool, src, dst):
     B, T = len(pool["lens"]), pool["T"]
     bad = any(not 0 <= r < B for r in [*src, *dst]) or len(set(dst)) < len(dst) or set(src) & set(dst)
-    if bad or any(pool["lens"][d] != 0 for d in dst):
+    if bad or any(length(pool, d) for d in dst):
         return -1, []
     free_pages = [p for p, n in enumerate(pool["refs"]) if n == 0]
     short = sum(length(pool, s) % T != 0 for s in src) - len(free_pages)
