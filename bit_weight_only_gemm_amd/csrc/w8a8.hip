@@ -1188,6 +1188,7 @@ struct GatedPlan {
   int rows, splits;
   int64_t tiles;
 };
+constexpr int64_t kSplit64 = 512, kSplit128 = 256;  // workgroups of a split call, at most
 GatedPlan plan_gated(int64_t M, int64_t F, int64_t K) {
   const int64_t N = 2 * F, KT = ceil_div(K, 128);
   GatedPlan best = {0, 1, 0};
@@ -1200,9 +1201,9 @@ GatedPlan plan_gated(int64_t M, int64_t F, int64_t K) {
   for (int s = 1; s <= 16 && (s == 1 || 4 * s <= KT); ++s) {
     const double steps = (double)ceil_div(KT, s);
     if (ceil_div(KT, ceil_div(KT, s)) != s) continue;  // a split would have none
-    if (s == 1 || t64 * s <= 512)
+    if (s == 1 || t64 * s <= kSplit64)
       offer(64, s, t64, 0.3 * steps * std::max(1.0, t64 * s / 256.0) + (s > 1 ? 1 + 1.2 * s : 0));
-    if (s == 1 || t128 * s <= 256)
+    if (s == 1 || t128 * s <= kSplit128)
       offer(128, s, t128, (t128 * s <= 256 ? 0.45 : 0.6 * ceil_div(t128 * s, 256)) * steps +
                               (s > 1 ? 4 + s : 0));
   }
@@ -1210,8 +1211,18 @@ GatedPlan plan_gated(int64_t M, int64_t F, int64_t K) {
   offer(256, 1, t256, 1.6 * KT * ceil_div(t256, 256));
   return best;
 }
-int64_t split_bytes(const GatedPlan& p) {
-  return p.splits == 1 ? 0 : pad256(p.tiles * 4) + p.splits * p.tiles * p.rows * p.rows * 4;
+// Bytes of the sums and counters of any plan for up to M tokens (a plan of fewer may
+// split K where that of more does not): plan_gated's limits on the tiles of a split call.
+int64_t split_bytes(int64_t M, int64_t F, int64_t K) {
+  const int64_t N = 2 * F, most = std::min<int64_t>(16, ceil_div(K, 128) / 4);
+  if (most < 2) return 0;
+  auto sums = [&](int64_t rows, int64_t limit) -> int64_t {
+    const int64_t column = ceil_div(N, rows);  // tiles of the least M
+    if (2 * column > limit) return 0;
+    return std::min(limit, ceil_div(M, rows) * column * most) * rows * rows * 4;
+  };
+  const int64_t bytes = std::max(sums(64, kSplit64), sums(128, kSplit128));
+  return bytes ? pad256(kSplit64 / 2 * 4) + bytes : 0;
 }
 
 template <int DT, int ACT, bool FUSED>
@@ -1324,7 +1335,7 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
 int64_t w8a8_gated_workspace_bytes(int64_t M, int64_t F, int64_t K) {
   if (F <= 0 || F > kMaxN || F % 8 != 0 || validate_shape(M, 2 * F, K) != W4A16_OK) return -1;
   if (fused_gated(M, F, K)) return 0;
-  return linear_bytes(M, K) + (few_gated(M, F, K) ? 0 : split_bytes(plan_gated(M, F, K)));
+  return linear_bytes(M, K) + (few_gated(M, F, K) ? 0 : split_bytes(M, F, K));
 }
 
 int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w_scale,

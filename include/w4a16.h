@@ -548,7 +548,8 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
  *        the exponential's argument; below 2^-126 |g| it may be 0.
  * Constraints and limits as for w8a8_gemm with N = 2 F, F % 8 == 0; the
  * workspace (codes of x, and sums where K is split over workgroups) as for
- * w8a8_linear, by w8a8_gated_workspace_bytes (-1 on bad input).  out must not
+ * w8a8_linear, by w8a8_gated_workspace_bytes (-1 on bad input; it does not fall
+ * as M grows, so one for the largest batch serves every smaller one).  out must not
  * lie between x's first and last value (W4A16_ERR_INVALID_ARG).  Async.
  * Bitwise reproducible, and a row of y does not depend on the other rows.
  */
