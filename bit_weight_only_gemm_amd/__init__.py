@@ -417,5 +417,5 @@ from .kv8 import (kv8_append, kv8_attention, kv8_attention_scored,  # noqa: E402
                   kv8_attention_workspace_bytes, kv8_cache, kv8_dequant)
 from .kv8_pages import (kv8_compact, kv8_copy_pages, kv8_fork, kv8_free,  # noqa: E402,F401
                         kv8_pages_workspace_bytes, kv8_refs, kv8_reserve)
-from .w8a8 import (w8a8_gated, w8a8_gated_workspace_bytes, w8a8_gemm,  # noqa: E402,F401
-                   w8a8_linear, w8a8_quantize, w8a8_workspace_bytes)
+from .w8a8 import (w8a8_gated, w8a8_gated_plan, w8a8_gated_workspace_bytes,  # noqa: E402,F401
+                   w8a8_gemm, w8a8_linear, w8a8_quantize, w8a8_workspace_bytes)

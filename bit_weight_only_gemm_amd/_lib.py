@@ -55,6 +55,7 @@ SIGNATURES = {
     "w8a8_gemm": (_c.c_int, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p]),
     "w8a8_linear": (_c.c_int, [_p, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p]),
     "w8a8_gated_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "w8a8_gated_plan": (_c.c_int, [_i64, _i64, _i64, _p, _i64, _p]),
     "w8a8_gated": (_c.c_int, [_p, _i64, _p, _p, _p, _i32, _p, _i64, _i64, _i64, _i32, _p, _i64,
                               _p]),
     "kv8_append": (_c.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _i32,

@@ -6,6 +6,9 @@
 //
 // The sum is exact in int32 (|c| <= 127 and K <= 2^17), so it does not depend
 // on any split of K.
+#include <stdio.h>
+#include <string.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -1336,6 +1339,28 @@ int64_t w8a8_gated_workspace_bytes(int64_t M, int64_t F, int64_t K) {
   if (F <= 0 || F > kMaxN || F % 8 != 0 || validate_shape(M, 2 * F, K) != W4A16_OK) return -1;
   if (fused_gated(M, F, K)) return 0;
   return linear_bytes(M, K) + (few_gated(M, F, K) ? 0 : split_bytes(M, F, K));
+}
+
+int w8a8_gated_plan(int64_t M, int64_t F, int64_t K, char* names_host, int64_t names_bytes,
+                    int64_t* names_len_host) {
+  return guarded([&]() -> int {
+    if (F <= 0 || F % 8 != 0) return W4A16_ERR_INVALID_ARG;
+    if (F > kMaxN) return W4A16_ERR_UNSUPPORTED;
+    if (int s = validate_shape(M, 2 * F, K)) return s;
+    if (names_bytes < 0 || (names_bytes > 0 && !names_host)) return W4A16_ERR_INVALID_ARG;
+    char names[96];
+    const char* quantize = fused_gated(M, F, K) ? "" : "w8a8_quantize_kernel + ";
+    const GatedPlan p = plan_gated(M, F, K);
+    if (few_gated(M, F, K))
+      snprintf(names, sizeof names, "%sw8a8_gated_stream_kernel", quantize);
+    else if (p.rows <= 128)
+      snprintf(names, sizeof names, "%sw8a8_tile_kernel %dx%d/%d", quantize, p.rows, p.rows, p.splits);
+    else
+      snprintf(names, sizeof names, "%sw8a8_wide_kernel %dx256", quantize, p.rows);
+    if (names_bytes > 0) snprintf(names_host, (size_t)names_bytes, "%s", names);
+    if (names_len_host) *names_len_host = (int64_t)strlen(names);
+    return W4A16_OK;
+  });
 }
 
 int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w_scale,

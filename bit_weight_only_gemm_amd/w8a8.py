@@ -14,7 +14,7 @@ or, for rows quantized once and used by several layers:
 
 import torch
 
-from . import _DT, _here, _lib, _need, _space_bytes, _stream, _ws_cache
+from . import _DT, _here, _lib, _names, _need, _space_bytes, _stream, _ws_cache
 
 _QDT = dict(_DT)
 _QDT[torch.float32] = 2
@@ -154,6 +154,12 @@ def w8a8_gated_workspace_bytes(M, F, K):
     if n < 0:
         raise _lib.W4A16Error("w8a8_gated_workspace_bytes: invalid shape M=%d F=%d K=%d" % (M, F, K))
     return n
+
+
+def w8a8_gated_plan(M, F, K):
+    """Kernels a w8a8_gated call of this shape launches (host-only query), with the
+    tiles' rows x columns and the workgroups that share a tile's K."""
+    return _names(_lib.lib().w8a8_gated_plan, M, F, K).split(" + ")
 
 
 def w8a8_gated(x, wq, w_scale, bias=None, act="silu", out=None, workspace=None, stream=None):

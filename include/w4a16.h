@@ -555,6 +555,11 @@ int w8a8_linear(const void* x, int64_t x_stride, const int8_t* wq, const float* 
  */
 typedef enum { W4A16_SILU = 0, W4A16_GELU = 1, W4A16_GELU_TANH = 2 } w4a16_act_t;
 int64_t w8a8_gated_workspace_bytes(int64_t M, int64_t F, int64_t K);
+/* Host-only plan query, as w4a16_gemm_plan: the kernels of a w8a8_gated call, with
+ * the rows x columns of their tiles and the workgroups that share a tile's K, e.g.
+ * "w8a8_quantize_kernel + w8a8_tile_kernel 64x64/4". */
+int w8a8_gated_plan(int64_t M, int64_t F, int64_t K, char* names_host, int64_t names_bytes,
+                    int64_t* names_len_host);
 int w8a8_gated(const void* x, int64_t x_stride, const int8_t* wq, const float* w_scale,
                const void* bias, int32_t act, void* out, int64_t M, int64_t F, int64_t K,
                int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream);
