@@ -114,9 +114,12 @@ def kv8_reserve(refs, page_table, seq_lens, added, page_size, status=None, works
     """Makes room for added (int32 [B]) more tokens in every row: takes the
     pages they need, the lowest free ones in the order of the rows, and adds
     them to seq_lens, as kv8_append wants it; below 0 drops that many last tokens
-    and gives back the pages that this empties.  Returns the status: 0, the pages
-    that are missing, or -1 where a row would pass the table's width, or after
-    dropping would end within a page that other rows hold too."""
+    and gives back the pages that this empties; the page that the row then ends in
+    keeps the scales and codes (a NaN too) that kv8_append made of the dropped rows
+    and those before them: drafts that must not show are appended to a fork.
+    Returns the status: 0, the pages that are missing, or -1 where a row would pass
+    the table's width, or after dropping would end within a page that other rows
+    hold too."""
     _need(refs, torch.int32, "refs")
     B, width = _rows(page_table, seq_lens)
     _need(added, torch.int32, "added", B)

@@ -773,6 +773,12 @@ int kv8_free(int32_t* refs, int64_t num_pages, int32_t page_size, int32_t* page_
  * need are taken, and seq_lens become the lengths with them.  Below 0 that many
  * last tokens are dropped (drafted ones; at most all), pages that this empties
  * are given back, to be taken from the next call on, and their entries become -1.
+ * A drop undoes no append: the page that the row then ends in keeps the scale that
+ * the dropped rows raised, the codes that its other rows were given under it, and a
+ * NaN scale (from an infinity or a NaN in a dropped row, for that head's every row
+ * of the page) until the page begins anew.  Where drafts must not show, fork the row
+ * (its partly filled page is copied), append them there, and free that row, or free
+ * this one in its place.
  * status -1: a row would pass max_pages * T, or end within a page that other
  * rows hold too (which the next append would change for them).
  */
