@@ -12,9 +12,9 @@
 // layers has 140 000 pages, 560 KB), and carried out by a second launch.
 //
 // The copies are bound by bytes (MI355X: compacting 1.17 GB of 4 caches 247 us, 4.7 TB/s,
-// the rate of a 4 GiB copy; a beam's step of 120 children over 16 caches, 302 MB, 76),
-// calls without many by their launches (3 to 9 us each) and the host's part: 27 us for
-// the free, fork and reserve of four beams.
+// the rate of a 4 GiB copy; a beam's step of 120 children over 16 caches, 302 MB, 76 to
+// 89 by card), calls without many by their launches (2 to 11 us each) and the host's
+// part: 27 us for the free, fork and reserve of four beams.
 #include <algorithm>
 
 #include "kv8.h"

@@ -638,7 +638,9 @@ int kv8_dequant(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_s
 
 /*
  * Workspace bytes of kv8_attention for these sizes (the partial results of
- * keys split over workgroups; 0 where none is split); -1 on bad input.
+ * keys split over workgroups; 0 where none is split); -1 on bad input.  Fewer
+ * sequences or tokens may need more, since their keys are split further: calls of
+ * several sizes take the largest of theirs.
  */
 int64_t kv8_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t max_new, int64_t max_len,
                                       int32_t H, int32_t Hkv, int32_t D);
@@ -696,11 +698,13 @@ int kv8_attention(const void* q, int64_t q_stride, const uint8_t* k_cache, const
  * query's `first`, or from every query's `end` on, are not read.  So several
  * documents in one sequence are kept apart by `first` when causal, and by `first`
  * and `end` where they are seen both ways: all of each (causal 0), or up to the
- * prefix.  A query that sees nothing gives 0 (and lse -inf).  Scores are fp32 in
- * all of this; the cap is off by 2^-20 softcap up to 350, by 2^-19 of the score
- * beyond.  Arguments, workspace (kv8_attention_workspace_bytes; it may be
- * kv8_attention's) and errors otherwise as for kv8_attention.  Async.  Bitwise
- * reproducible.
+ * prefix.  first and prefix without end are no document mask.  A query that sees
+ * nothing gives 0 (and lse -inf).  Scores are fp32 in all of this; the cap is off by
+ * 2^-20 softcap up to 350, by 2^-19 of the score beyond.  Probabilities enter the
+ * second product as fp16 and queries as fp16, with kv8_attention's errors (fp16
+ * results are 2.8e-4 off, relative RMS, where rounding alone is 2.0e-4).  Arguments,
+ * workspace (kv8_attention_workspace_bytes; it may be kv8_attention's) and errors
+ * otherwise as for kv8_attention.  Async.  Bitwise reproducible.
  */
 int kv8_attention_scored(const void* q, int64_t q_stride, const uint8_t* k_cache,
                          const uint8_t* v_cache, const float* k_scale, const float* v_scale,
