@@ -392,7 +392,8 @@ def nf4_dequant(nf4, dtype=torch.bfloat16, stream=None):
 # calls on that stream (calls on one stream run in order; the kernels write
 # every workspace byte they read, so its contents do not matter).  One that is
 # outgrown keeps its memory, since a graph captured on the stream goes on writing
-# there; sizes at least double, so that all of these are less than the last.
+# there; sizes at least double where memory allows, so that all of these are less than
+# the last.
 _WS = {}
 _OUTGROWN = []
 
@@ -404,12 +405,15 @@ def _ws_cache(device, nbytes, stream=None, kept=None):
     if cur is None or cur.numel() * 4 < nbytes:
         st = torch.cuda.current_stream() if stream is None else stream
         st.synchronize()
+        ample = max(nbytes, 1 << 20 if cur is None else 8 * cur.numel())
+        with torch.cuda.stream(st):     # a block of the stream that uses it
+            try:
+                new = workspace(ample, device)
+            except torch.OutOfMemoryError:
+                new = workspace(nbytes, device)
         if cur is not None:
             _OUTGROWN.append(cur)
-            nbytes = max(nbytes, 8 * cur.numel())
-        with torch.cuda.stream(st):     # a block of the stream that uses it
-            cur = workspace(max(nbytes, 1 << 20), device)
-        kept[key] = cur
+        kept[key] = cur = new
     return cur
 
 

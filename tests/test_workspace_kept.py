@@ -45,3 +45,22 @@ def test_growing_in_small_steps_keeps_little():
         if not sizes or sizes[-1] != w.numel():
             sizes.append(w.numel())
     assert sum(sizes) <= 2 * sizes[-1] and sizes[-1] * 4 <= 2 * (39 << 20)
+
+
+def test_what_does_not_fit_twice_is_made_as_large_as_needed(monkeypatch):
+    made = []
+
+    def limited(nbytes, device):
+        if nbytes > 5 << 20:
+            raise torch.OutOfMemoryError
+        made.append(nbytes)
+        return torch.zeros(nbytes // 4, dtype=torch.int32)
+
+    monkeypatch.setattr(w4, "workspace", limited)
+    kept, device = {}, torch.device("cpu")
+    for need in (3 << 20, 4 << 20):
+        assert w4._ws_cache(device, need, Stream(), kept).numel() * 4 >= need
+    assert made == [3 << 20, 4 << 20]
+    with pytest.raises(torch.OutOfMemoryError):
+        w4._ws_cache(device, 6 << 20, Stream(), kept)
+    assert w4._ws_cache(device, 4 << 20, Stream(), kept).numel() * 4 == 4 << 20
