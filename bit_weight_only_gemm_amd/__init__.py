@@ -404,6 +404,11 @@ def _ws_cache(device, nbytes, stream=None, kept=None):
     cur = kept.get(key)
     if cur is None or cur.numel() * 4 < nbytes:
         st = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(st):
+            if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+                raise W4A16Error("no workspace of %d bytes is kept for this stream, and none can be "
+                                 "made in a capture: pass one, or make the call on the stream "
+                                 "before it is captured" % nbytes)
         st.synchronize()
         ample = max(nbytes, 1 << 20 if cur is None else 8 * cur.numel())
         with torch.cuda.stream(st):     # a block of the stream that uses it

@@ -165,7 +165,8 @@ def kv8_attention(q, cache, page_table, seq_lens, cu_seqlens=None, max_new=None,
     keys are chosen: pass them where cu_seqlens is.  Rows past max_new are not
     processed.  lse: fp32 [tokens, H], written if given.  workspace: one of
     kv8_attention_workspace_bytes, kept for these calls alone and zero before
-    the first (one per stream is kept when not given): it holds counters, and
+    the first (one per stream is kept when not given; a call that is captured
+    finds it there from a call before, or is given one): it holds counters, and
     one that another operator has written in leaves results unwritten."""
     return _attention("kv8_attention", None, q, cache, page_table, seq_lens, cu_seqlens, max_new,
                       max_len, scale, causal, out, lse, workspace, stream)

@@ -15,7 +15,8 @@ Nothing is read back to the host, so the calls can be captured in a graph; what
 may fail on the device says so in a status tensor (int32 [1]): 0 done, above 0
 the pages that were missing, -1 rows that the call refuses; then nothing has
 been changed.  Calls that overlap in time must not share a workspace (one per
-stream is kept when none is given).
+stream is kept when none is given; a call that is captured finds it there from a
+call before, or is given one).
 """
 
 import ctypes

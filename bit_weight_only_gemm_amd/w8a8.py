@@ -169,7 +169,8 @@ def w8a8_gated(x, wq, w_scale, bias=None, act="silu", out=None, workspace=None, 
     "silu", "gelu" (with the error function) or "gelu_tanh".  workspace: one of
     w8a8_gated_workspace_bytes (kept per stream when not given); it is written
     over, so never kv8_attention's, and calls that overlap in time (graphs
-    replayed side by side) must not share one.  out must not overlap x."""
+    replayed side by side) must not share one; a call that is captured finds the
+    kept one there from a call before, or is given one.  out must not overlap x."""
     if act not in _ACT:
         raise ValueError("act must be one of %s, got %r" % (", ".join(_ACT), act))
     N, K = _weights(wq, w_scale, bias, x.dtype)
