@@ -500,7 +500,7 @@ w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
 // 55296 x 5120 in 1850 to 1950 us by card, 2.5 to 2.4 PFLOP/s, the units busy 68 %
 // of the cycles (2.57 with every load from L2, 2.82 without loads; with one tile
 // per workgroup and loads straight to LDS it took 2324 us).  The gated form of it, 8192
-// x 27648 x 5120, takes 1893 to 2010 us by card, its quantizing among them: half the
+// x 27648 x 5120, takes 1893 to 2048 us by card, its quantizing among them: half the
 // results to write pay for the activations.
 constexpr int kWideStage = 512 * 128, kWideTurn = 2 * kWideStage, kWideScales = kWideTurn + 4 * 4096;
 // x's scales, w's, the bias as fp32; of this tile and of the one before
